@@ -356,6 +356,74 @@ MXG_API int bf16_gemm_small_ex(const void *X, const void *W, int M, int N, int K
                void *workspace, size_t workspace_bytes, const mxg_gemm_options *opts,
                cudaStream_t stream);
 
+/* ------------------------------------------------- low-rank adapters */
+
+/* Adapters of many requests at once on the output of a projection that they
+ * share (any of the GEMMs above):
+ *     Out[m] = Y[m] + scales[a] * (X[m] * A[a]^T) * B[a]^T,  a = index[m].
+ * A token whose index is outside 0 .. L-1 has no adapter: Out[m] = Y[m].
+ *   X       device, bf16 [M][K], rows ldx elements apart (the projection's
+ *           input);
+ *   A       device, bf16 [L][R][K]; B device, bf16 [L][N][R]: the adapters'
+ *           two factors, a smaller rank padded with zeros;
+ *   scales  device, fp32 [L], or NULL for 1 (4-byte aligned);
+ *   index   device, int32 [M], in any order (4-byte aligned);
+ *   Y, Out  device, bf16 [M][N], rows ldy and ldo elements apart: a column
+ *           range of a fused projection's output will do.  Out may be Y
+ *           itself (then ldo = ldy), which this call exempts from the
+ *           no-alias rule; otherwise the two must not overlap;
+ *   workspace  device, lora_workspace_bytes(M, N, K, R) bytes for the inner
+ *           products X * A^T; needs no initialisation and keeps nothing that
+ *           a later call reads.  Not the workspace of a call that may run at
+ *           the same time.
+ * The inner products are held to 16 bits of mantissa at least (not rounded to
+ * bf16), sums in fp32; Out is rounded once.  Bitwise reproducible.  Unlike the
+ * GEMMs, nothing is read before the previous kernel on `stream` has
+ * completed: A, B and index may be what it writes.
+ * 1 <= M <= 2097088; K, N, R >= 8 and multiples of 8; R <= 128;
+ * strides multiples of 8.  Other sizes: MXG_ERR_UNSUPPORTED_SHAPE; a stride
+ * below its row or not a multiple of 8, L < 1: MXG_ERR_INVALID_ARG. */
+MXG_API size_t lora_workspace_bytes(int M, int N, int K, int R);
+MXG_API int lora_add(const void *X, long long ldx, const void *A, const void *B,
+               const float *scales, const int *index, const void *Y, long long ldy, void *Out,
+               long long ldo, int M, int N, int K, int R, int L, void *workspace,
+               size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- sampling */
+
+/* One token per row of logits (the output of a vocabulary head), from a given
+ * random number, after the filters of the Eole recipe (section "Sample with
+ * MTP": temperature, then top-p, then top-k) and min-p.  For a row with
+ * logits l, T = temperature, w_i = exp((l_i - max l) / T), its entries ranked
+ * by falling l (equal ones by rising index), the tokens kept are those with
+ *     mass of the higher-ranked tokens < top_p * (sum of all w),
+ *     rank < top_k (ranks from 0), and
+ *     l_i - max l >= T * ln(min_p)          (w_i >= min_p);
+ * the first-ranked one always is.  The token is the first in index order for
+ * which the kept mass up to and including it exceeds u * (whole kept mass);
+ * u >= 1 or NaN gives the last kept one, u < 0 the first.
+ *   logits  device, bf16 (MXG_DTYPE_BF16) or fp32 (MXG_DTYPE_FP32), [M][V],
+ *           rows ld >= V elements apart, aligned to their type only;
+ *   u       device, fp32 [M];
+ *   temperature, top_p, min_p  device, fp32 [M] each, or NULL;
+ *   top_k   device, int32 [M], or NULL;
+ *   tokens  device, int32 [M]; probs device, fp32 [M], or NULL: the token's
+ *           share of the kept mass.
+ * Off: temperature NULL is 1; top_k <= 0, top_p >= 1 or NaN, min_p <= 0 or
+ * NaN.  Temperature <= 0 or NaN: the lowest index of the row's maximum, with
+ * probability 1.  Entries of -inf or NaN are never taken; when a row holds
+ * nothing else, its token is -1 and its probability 0.  With entries of
+ * +inf, those share the mass equally and no other has any.
+ * Masses are summed as integers in units of 2^-44 of the largest weight, each
+ * from a weight in fp64: the result does not depend on the order of sums.
+ * A share below 2^-45 counts as none.
+ * 1 <= V <= 393216 and M <= 2^27, else MXG_ERR_UNSUPPORTED_SHAPE.  Reads nothing before the
+ * previous kernel on `stream` has completed. */
+enum { MXG_DTYPE_BF16 = 0, MXG_DTYPE_FP32 = 1 };
+MXG_API int sample_logits(const void *logits, int dtype, long long ld, int M, int V,
+               const float *u, const float *temperature, const int *top_k, const float *top_p,
+               const float *min_p, int *tokens, float *probs, cudaStream_t stream);
+
 /* --------------------------------------------------- test and diagnostics */
 
 /* Decode a re-packed INT4 buffer with the device routines of the GEMM paths.

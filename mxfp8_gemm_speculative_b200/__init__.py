@@ -1,4 +1,5 @@
-"""Python binding of libmxg.so: weight-quantized linear layer on B200.
+"""Python binding of libmxg.so: weight-quantized linear layer on B200, the
+adapters beside it and the sampler behind its head.
 
     Y[M][N] = X[M][K] * dequant(W)^T     bf16 activations, fp32 accumulate, bf16 out
 
@@ -35,6 +36,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 _SIGS = {
     "mxg_status_string": (ctypes.c_char_p, [_i]),
@@ -68,6 +70,9 @@ _SIGS = {
     "bf16_gemm_small_workspace_bytes": (_sz, [_i, _i, _i]),
     "bf16_gemm_small": (_i, [_p, _p, _i, _i, _i, _p, _p, _sz, _p]),
     "bf16_gemm_small_ex": (_i, [_p, _p, _i, _i, _i, _p, _p, _sz, _p, _p]),
+    "lora_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "lora_add": (_i, [_p, _ll, _p, _p, _p, _p, _p, _ll, _p, _ll, _i, _i, _i, _i, _i, _p, _sz, _p]),
+    "sample_logits": (_i, [_p, _i, _ll, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -85,6 +90,7 @@ MXG_ERR_TIMEOUT = -5
 MXG_ERR_CAPTURE = -6
 
 PATH_AUTO, PATH_STREAM, PATH_TENSOR = 0, 1, 2
+DTYPE_BF16, DTYPE_FP32 = 0, 1
 
 
 class GemmOptions(ctypes.Structure):
@@ -687,6 +693,203 @@ def bf16_gemm_small(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None =
               _ptr(out), _ptr(ws), ws.numel(), _options(PATH_AUTO, late_weights),
               stream=stream)
     return out
+
+
+# ------------------------------------------------------- low-rank adapters
+def _need_rows(t: torch.Tensor, M: int, N: int, device, name: str) -> int:
+    """The row stride of a bf16 [M][N] whose rows are contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != N:
+        raise ValueError(f"{name} must be [{M}][{N}], got {list(t.shape)}")
+    _same_device(t, device, name)
+    if N > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if M == 1:
+        return -(-N // 8) * 8      # one row: its stride says nothing
+    return t.stride(0)
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor, lda: int, ldb: int) -> bool:
+    """Do the [M][N] of two tensors (2 bytes an element) share memory?  Column
+    ranges of one buffer with one row stride do not, when their columns
+    differ."""
+    M, N = a.shape
+    pa, pb = a.data_ptr(), b.data_ptr()
+    if pa >= pb + 2 * ((M - 1) * ldb + N) or pb >= pa + 2 * ((M - 1) * lda + N):
+        return False
+    if lda != ldb:
+        return True
+    d = (pa - pb) % (2 * lda)
+    return d < 2 * N or 2 * lda - d < 2 * N
+
+
+def _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream):
+    """The arguments of the C call, and the tensors behind them."""
+    dev = x.device
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a must be [L][R][K] and b [L][N][R]")
+    L, R, K = a.shape
+    N = b.shape[1]
+    if b.shape[0] != L or b.shape[2] != R:
+        raise ValueError(f"b must be [{L}][N][{R}], got {list(b.shape)}")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M][{K}], got {list(x.shape)}")
+    M = x.shape[0]
+    _need(a, torch.bfloat16, "a")
+    _need(b, torch.bfloat16, "b")
+    _need(index, torch.int32, "index")
+    if index.dim() != 1 or index.shape[0] != M:
+        raise ValueError(f"index must be [{M}], got {list(index.shape)}")
+    ldx = _need_rows(x, M, K, dev, "x")
+    ldy = _need_rows(y, M, N, dev, "y")
+    for t, name in ((a, "a"), (b, "b"), (index, "index")):
+        _same_device(t, dev, name)
+    if scales is not None:
+        _need(scales, torch.float32, "scales")
+        if scales.dim() != 1 or scales.shape[0] != L:
+            raise ValueError(f"scales must be [{L}], got {list(scales.shape)}")
+        _same_device(scales, dev, "scales")
+    need = lora_workspace_bytes(M, N, K, R)
+    if need == 0:
+        raise MxgError(MXG_ERR_UNSUPPORTED_SHAPE, "lora_add")
+    if out is None:
+        out = _empty((M, N), torch.bfloat16, dev, stream)
+        ldo = N
+    else:
+        ldo = _need_rows(out, M, N, dev, "out")
+        same = out.data_ptr() == y.data_ptr() and ldo == ldy
+        if not same and _overlap(out, y, ldo, ldy):
+            raise ValueError("out must be y or not overlap it")
+    if workspace_buf is None:
+        # this call's own, from the stream's pool: calls captured into
+        # different graphs never share it
+        ws = _empty(need, torch.uint8, dev, stream)
+    else:
+        ws = workspace_buf
+        _need_ws(ws, dev)
+    args = (_ptr(x), ldx, _ptr(a), _ptr(b), _ptr(scales), _ptr(index), _ptr(y), ldy, _ptr(out),
+            ldo, M, N, K, R, L, _ptr(ws), ws.numel())
+    return args, out, (x, a, b, scales, index, y, out, ws, stream)
+
+
+def lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
+    return int(_lib.lora_workspace_bytes(M, N, K, R))
+
+
+def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor,
+             y: torch.Tensor, scales: torch.Tensor | None = None,
+             out: torch.Tensor | None = None, workspace_buf: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """Low-rank adapters of many requests on the output ``y`` [M][N] of a
+    projection they share: out[m] = y[m] + scales[i] * (x[m] a[i]^T) b[i]^T
+    with i = index[m], for x bf16 [M][K], a bf16 [L][R][K], b bf16 [L][N][R],
+    scales fp32 [L] (None: 1) and index int32 [M]; a token whose index is
+    outside 0 .. L-1 (say -1) keeps its y.  ``out=y`` adds in place.  The rows
+    of x, y and out may be strided (a column range of a fused projection)."""
+    args, out, keep = _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream)
+    _dev_call(x.device, "lora_add", _lib.lora_add, *args, stream=stream)
+    return out
+
+
+def prepare_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor,
+                     y: torch.Tensor, scales: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, workspace_buf: torch.Tensor | None = None,
+                     stream=None):
+    """(call, out): ``call()`` runs lora_add on these buffers into ``out``."""
+    args, out, keep = _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream)
+    return PreparedCall(_lib.lora_add, args + (_stream(stream, x.device),), "lora_add", keep,
+                        x.device), out
+
+
+# ---------------------------------------------------------------- sampling
+def _sample_args(logits, u, temperature, top_k, top_p, min_p, tokens, probs, stream):
+    """The arguments of the C call, its outputs, and the tensors behind them."""
+    dev = logits.device
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [M][V], got {list(logits.shape)}")
+    M, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("the rows of logits must be contiguous")
+    ld = logits.stride(0) if M > 1 else V
+    if u is None:
+        raise ValueError("u must be given: one random number per row")
+    given = ((u, torch.float32, "u"), (temperature, torch.float32, "temperature"),
+             (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"),
+             (min_p, torch.float32, "min_p"), (tokens, torch.int32, "tokens"),
+             (probs, torch.float32, "probs"))
+    for t, dtype, name in given:
+        if t is None:
+            continue
+        _need(t, dtype, name)
+        if t.dim() != 1 or t.shape[0] != M:
+            raise ValueError(f"{name} must be [{M}], got {list(t.shape)}")
+        _same_device(t, dev, name)
+    if tokens is None:
+        tokens = _empty((M,), torch.int32, dev, stream)
+    if probs is None:
+        probs = _empty((M,), torch.float32, dev, stream)
+    args = (_ptr(logits), DTYPE_BF16 if logits.dtype == torch.bfloat16 else DTYPE_FP32, ld, M, V,
+            _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens),
+            _ptr(probs))
+    return args, (tokens, probs), (logits, u, temperature, top_k, top_p, min_p, tokens, probs,
+                                   stream)
+
+
+def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
+                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                  min_p: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                  probs: torch.Tensor | None = None, stream=None):
+    """(tokens int32 [M], probs fp32 [M]): one token per row of logits (bf16
+    or fp32 [M][V], rows may be strided) from the random numbers u fp32 [M],
+    after each row's temperature (<= 0: greedy), top_p, top_k and min_p ([M]
+    each, None: off), and its share of the mass those filters keep.  The
+    definition, with its order of filters and ties, is in include/mxg.h."""
+    args, outs, keep = _sample_args(logits, u, temperature, top_k, top_p, min_p, tokens, probs,
+                                    stream)
+    _dev_call(logits.device, "sample_logits", _lib.sample_logits, *args, stream=stream)
+    return outs
+
+
+def prepare_sample_logits(logits: torch.Tensor, u: torch.Tensor,
+                          temperature: torch.Tensor | None = None,
+                          top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                          min_p: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                          probs: torch.Tensor | None = None, stream=None):
+    """(call, (tokens, probs)): ``call()`` runs sample_logits on these buffers."""
+    args, outs, keep = _sample_args(logits, u, temperature, top_k, top_p, min_p, tokens, probs,
+                                    stream)
+    return PreparedCall(_lib.sample_logits, args + (_stream(stream, logits.device),),
+                        "sample_logits", keep, logits.device), outs
+
+
+def w8a16_gemm_sample(x: torch.Tensor, packed: torch.Tensor, N: int, K: int, u: torch.Tensor,
+                      temperature: torch.Tensor | None = None, top_k: torch.Tensor | None = None,
+                      top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+                      group_size: int = 128, vocab: int | None = None,
+                      logits: torch.Tensor | None = None,
+                      workspace_buf: torch.Tensor | None = None, stream=None):
+    """The INT8 vocabulary head and the sampler on its logits: (tokens, probs,
+    logits) for x bf16 [M][K] (M <= 32) and w8a16_repack's buffer.  ``vocab``
+    (default N) is the number of real columns of a head padded to N; only
+    those are sampled."""
+    V = N if vocab is None else int(vocab)
+    if not 1 <= V <= N:
+        raise ValueError(f"vocab must be in 1 .. {N}, got {V}")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M][{K}], got {list(x.shape)}")
+    if logits is None:
+        logits = _empty((x.shape[0], N), torch.bfloat16, x.device, stream)
+    _need_out(logits, x.shape[0], N, x.device)
+    # the sampler's arguments are looked at before the head runs
+    args, outs, keep = _sample_args(logits[:, :V], u, temperature, top_k, top_p, min_p, None,
+                                    None, stream)
+    w8a16_gemm(x, packed, N, K, group_size, out=logits, workspace_buf=workspace_buf,
+               stream=stream)
+    _dev_call(x.device, "sample_logits", _lib.sample_logits, *args, stream=stream)
+    return *outs, logits
 
 
 def mxg_selftest_wait_timeout(workspace_buf: torch.Tensor | None, limit_us: int,

@@ -129,6 +129,26 @@ cudaError_t launch_pdl(const void *fn, dim3 grid, dim3 block, size_t smem, cudaS
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+cudaError_t launch_pdl_cluster(const void *fn, dim3 grid, dim3 block, int cluster, size_t smem,
+                               cudaStream_t stream, void **args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
 // Workspace needs of the two paths for one shape (0 when the path cannot run it).
 static size_t w4a16_stream_ws(int dev, int M, int N, int K, int G)
 {
@@ -518,6 +538,61 @@ int mxfp8_gemm_packed(const void *X, const void *packed, int M, int N, int K, vo
                       void *workspace, size_t workspace_bytes, cudaStream_t stream)
 {
     return mxfp8_gemm_packed_ex(X, packed, M, N, K, Y, workspace, workspace_bytes, nullptr, stream);
+}
+
+namespace {
+bool aligned4(const void *p)
+{
+    return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+}  // namespace
+
+size_t lora_workspace_bytes(int M, int N, int K, int R)
+{
+    return lora_shape_ok(M, N, K, R) ? lora_scratch_bytes(M, R) : 0;
+}
+
+int lora_add(const void *X, long long ldx, const void *A, const void *B, const float *scales,
+             const int *index, const void *Y, long long ldy, void *Out, long long ldo, int M, int N,
+             int K, int R, int L, void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || !aligned16(Out) ||
+        !aligned16(workspace) || !aligned4(index) || (scales && !aligned4(scales)) || M < 1 || L < 1)
+        return MXG_ERR_INVALID_ARG;
+    if (ldx < K || ldy < N || ldo < N || ldx % 8 || ldy % 8 || ldo % 8 || (Out == Y && ldo != ldy))
+        return MXG_ERR_INVALID_ARG;
+    if (!lora_shape_ok(M, N, K, R))
+        return MXG_ERR_UNSUPPORTED_SHAPE;
+    if (workspace_bytes < lora_scratch_bytes(M, R))
+        return MXG_ERR_WORKSPACE;
+    const int dev = current_device();
+    if (dev < 0)
+        return MXG_ERR_CUDA;
+    const LoraPlan pl = plan_lora(dev, M, N, K, R);
+    const LoraArgs a{X, A, B, Y, Out, scales, index, ldx, ldy, ldo, M, N, K, R, L, workspace};
+    return to_status(launch_lora(pl, a, stream));
+}
+
+int sample_logits(const void *logits, int dtype, long long ld, int M, int V, const float *u,
+                  const float *temperature, const int *top_k, const float *top_p,
+                  const float *min_p, int *tokens, float *probs, cudaStream_t stream)
+{
+    if (dtype != MXG_DTYPE_BF16 && dtype != MXG_DTYPE_FP32)
+        return MXG_ERR_INVALID_ARG;
+    const bool fp32 = dtype == MXG_DTYPE_FP32;
+    if (!logits || (reinterpret_cast<uintptr_t>(logits) & (fp32 ? 3u : 1u)) || !aligned4(u) ||
+        (temperature && !aligned4(temperature)) || (top_k && !aligned4(top_k)) ||
+        (top_p && !aligned4(top_p)) || (min_p && !aligned4(min_p)) || !aligned4(tokens) ||
+        (probs && !aligned4(probs)) || M < 1 || ld < V)
+        return MXG_ERR_INVALID_ARG;
+    if (!sample_shape_ok(M, V))
+        return MXG_ERR_UNSUPPORTED_SHAPE;
+    const int dev = current_device();
+    if (dev < 0)
+        return MXG_ERR_CUDA;
+    const SamplePlan pl = plan_sample(dev, M, V, fp32);
+    const SampleArgs a{logits, fp32, ld, M, V, u, temperature, top_p, min_p, top_k, tokens, probs};
+    return to_status(launch_sample(pl, a, stream));
 }
 
 int w4a16_unpack(const void *packed, int K, int N, int group_size, uint8_t *codes, float *w_fp32,

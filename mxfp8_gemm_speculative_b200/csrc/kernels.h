@@ -106,6 +106,51 @@ bool plan_bf16_small(int M, int N, int K, SmallPlan *plan);
 cudaError_t launch_bf16_small(const SmallPlan &plan, const void *X, const void *W, int M, int N,
                               int K, void *Y, void *workspace, bool early, cudaStream_t stream);
 
+// ------------------------------------------------------ low-rank adapters
+struct LoraPlan {
+    int blocks;           // blocks of 64 tokens
+    int rank_tiles;       // 16-rank tiles a shrink CTA holds (1, 2, 4)
+    int slices;           // rank slices of that many tiles
+    int cluster;          // CTAs that split K (shrink)
+    int shrink_subs, expand_subs;   // CTAs that share a block's groups
+    int expand_warps;     // warps (of 32 columns) per expand CTA
+    int ntiles;           // column tiles (expand)
+};
+struct LoraArgs {
+    const void *X, *A, *B, *Y;
+    void *Out;
+    const float *scales;  // or NULL
+    const int *index;
+    long long ldx, ldy, ldo;
+    int M, N, K, R, L;
+    void *workspace;
+};
+bool lora_shape_ok(int M, int N, int K, int R);
+size_t lora_scratch_bytes(int M, int R);   // the [M][R] inner products
+LoraPlan plan_lora(int device, int M, int N, int K, int R);   // of a shape that is ok
+cudaError_t launch_lora(const LoraPlan &plan, const LoraArgs &args, cudaStream_t stream);
+
+// --------------------------------------------------------------- sampling
+struct SamplePlan {
+    int cluster;          // CTAs per row
+    int per;              // entries per CTA
+    int threads;
+    size_t smem;
+};
+struct SampleArgs {
+    const void *logits;
+    bool fp32;            // else bf16
+    long long ld;
+    int M, V;
+    const float *u, *temperature, *top_p, *min_p;   // parameters: [M] or NULL
+    const int *top_k;                               // [M] or NULL
+    int *tokens;
+    float *probs;
+};
+bool sample_shape_ok(int M, int V);
+SamplePlan plan_sample(int device, int M, int V, bool fp32);   // of a shape that is ok
+cudaError_t launch_sample(const SamplePlan &plan, const SampleArgs &args, cudaStream_t stream);
+
 // ------------------------------------------------------------ weight tools
 // n_major: compressed-tensors inputs ([N][K/8] words, [N][K/G] scales)
 // instead of GPTQ's ([K/8][N], [K/G][N]).
@@ -141,6 +186,10 @@ size_t static_scratch_bytes();
 // before touching anything that kernel could have written).
 cudaError_t launch_pdl(const void *fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        void **args);
+
+// The same with thread-block clusters of `cluster` CTAs along x.
+cudaError_t launch_pdl_cluster(const void *fn, dim3 grid, dim3 block, int cluster, size_t smem,
+                               cudaStream_t stream, void **args);
 
 // Encodes tensor maps through the driver entry point (no libcuda link).
 bool encode_tensor_map_2d(void *map, int dtype_cu, const void *base, uint64_t inner,
