@@ -228,11 +228,22 @@ __device__ __forceinline__ uint32_t cluster_size()
 
 // Barrier over the cluster's threads: shared memory written before it is
 // visible to the peers' loads after it.
-__device__ __forceinline__ void cluster_barrier()
+__device__ __forceinline__ void cluster_arrive()
 {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    cluster_arrive();
+    cluster_wait();
 }
 
 // Address of the same shared-memory object in CTA `rank` of the cluster.

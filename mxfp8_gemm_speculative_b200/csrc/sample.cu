@@ -17,14 +17,15 @@
 //    token.  fp32 weights would not do: a token is picked where a running sum
 //    of up to 248320 terms crosses a border, and an error of 2^-22 moves
 //    that border past whole tokens.
-//  * The kept set is a cut (key, ties): every entry above a logit value, and
-//    the first few in index order of those equal to it (bf16 logits tie by
-//    the thousand).  It is found by histograms: 512 bins of 1/16 binade of
+//  * The kept set is a cut (value, ties): every entry above a logit value,
+//    and the first few in index order of those equal to it (bf16 logits tie
+//    by the thousand).  It is found by histograms: 512 bins of 1/16 binade of
 //    the weight first, over all entries, then only over the entries of the
 //    bin in which the border falls, 512 bins of their key range at a time,
 //    until a bin is a single key.  No sort.
 //  * One last pass adds the kept weights per warp segment in index order; the
-//    warp in whose segment u * (kept mass) falls walks its entries.
+//    CTA, the warp and the lane in whose part u * (kept mass) falls are found
+//    from the sums of the parts, and only that part is looked through.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -44,6 +45,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = 32;
 constexpr int kFix = 44;          // weights are multiples of 2^-kFix
 constexpr int kSmemSlice = 192 * 1024;   // most bytes of logits a CTA holds
+constexpr int kSlack = 136;       // slots beyond a CTA's entries: skew and the last 128
 
 struct SampleParams {
     const void *logits;
@@ -56,14 +58,43 @@ struct SampleParams {
 };
 
 // ------------------------------------------------------------------ entries
-// The value of stored bits: NaN becomes -inf and -0 becomes +0.
+// A CTA's entries lie in shared memory in slots: [0, skew) and those behind
+// the last entry hold -inf, so that every loop runs over whole groups of
+// four.  NaN is stored as -inf and -0 as +0.
+__device__ __forceinline__ float canonical(float v)
+{
+    return fmaxf(v, -INFINITY) + 0.f;
+}
 __device__ __forceinline__ float value_of(uint16_t b)
 {
-    return fmaxf(__uint_as_float((uint32_t)b << 16), -INFINITY) + 0.f;
+    return __uint_as_float((uint32_t)b << 16);
 }
 __device__ __forceinline__ float value_of(uint32_t b)
 {
-    return fmaxf(__uint_as_float(b), -INFINITY) + 0.f;
+    return __uint_as_float(b);
+}
+template <typename T>
+__device__ __forceinline__ T bits_of(float v)
+{
+    return sizeof(T) == 2 ? (T)(__float_as_uint(v) >> 16) : (T)__float_as_uint(v);
+}
+
+// Four consecutive slots.
+__device__ __forceinline__ void load4(const uint16_t *d, int slot, float (&v)[4])
+{
+    const uint2 w = *reinterpret_cast<const uint2 *>(d + slot);
+    v[0] = __uint_as_float(w.x << 16);
+    v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(w.y << 16);
+    v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load4(const uint32_t *d, int slot, float (&v)[4])
+{
+    const float4 w = *reinterpret_cast<const float4 *>(d + slot);
+    v[0] = w.x;
+    v[1] = w.y;
+    v[2] = w.z;
+    v[3] = w.w;
 }
 
 // Integer keys that rise with the value; those of bf16 have 16 bits.
@@ -86,48 +117,63 @@ __device__ __forceinline__ float key_value(uint32_t k, uint32_t)
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// Weights of one row: round(2^kFix * exp((v - top) / T)).
+// Weights of one row, round(2^kFix * exp((v - top) / T)), for finite v.
 struct Weights {
-    float top;
-    double dtop;
-    double c;             // 256 * log2(e) / T
-    const double *table;  // 2^(j / 256)
+    float least;          // 48 binades below the top or lower: no weight
+    double top;
+    double c;             // 64 * log2(e) / T
+    const double *table;  // 2^(j / 64)
 
-    __device__ __forceinline__ u64 operator()(float v) const
+    // (v - top) / T in units of 1/64 binade, its integer part in the low bits
+    __device__ __forceinline__ double scaled(float v, double &d) const
     {
-        if (v == top)
-            return 1ull << kFix;   // also for +inf
-        // (v - top) / T in units of 1/256 binade, not below -70 binades
-        // (smaller weights round to none, and so does everything beside an
-        // infinite top); split into an integer and a rest f in [-1/2, 1/2]
-        const double x = fmax(((double)v - dtop) * c, -70.0 * 256.0);
         constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52
-        const double m = x + kMagic;
+        d = (double)fmaxf(v, least) - top;
+        return fma(d, c, kMagic);
+    }
+
+    // First-level bin: 1/16 binade of the weight, the last bin holding
+    // everything from 32 binades down.  It never falls as v falls.
+    __device__ __forceinline__ int bin(double m) const
+    {
+        return min(-__double2loint(m) >> 2, kBins - 1);
+    }
+
+    __device__ __forceinline__ int bin(float v) const
+    {
+        double d;
+        return bin(scaled(v, d));
+    }
+
+    __device__ __forceinline__ u64 weight(double m, double d) const
+    {
+        constexpr double kMagic = 6755399441055744.0;
         const int n = __double2loint(m);
-        const double f = x - (m - kMagic);
-        // 2^(f / 256) - 1 by its series: |f ln2 / 256| <= 0.00136, so the
-        // fifth-order term is below 2^-54
-        constexpr double l = 0.69314718055994530942 / 256.0;
+        const double f = fma(d, c, -(m - kMagic));
+        // 2^(f / 64) - 1 by its series: |f| <= 1/2, |f ln2 / 64| <= 0.0055,
+        // so the sixth-order term is below 2^-54
+        constexpr double l = 0.69314718055994530942 / 64.0;
         const double q =
-            f * (l + f * (l * l / 2.0 + f * (l * l * l / 6.0 + f * (l * l * l * l / 24.0))));
-        const double t = table[n & 255];
+            f * (l + f * (l * l / 2.0 +
+                          f * (l * l * l / 6.0 +
+                               f * (l * l * l * l / 24.0 + f * (l * l * l * l * l / 120.0)))));
+        const double t = table[n & 63];
         const double w = fma(t, q, t);
-        // times 2^(n / 256 + kFix) by the exponent field, then rounded to an
+        // times 2^(n / 64 + kFix) by the exponent field, then rounded to an
         // integer by adding 2^52
-        const double s = __hiloint2double(__double2hiint(w) + (((n >> 8) + kFix) << 20),
+        const double s = __hiloint2double(__double2hiint(w) + (((n >> 6) + kFix) << 20),
                                           __double2loint(w));
         const double r = s + 4503599627370496.0;
         return (u64)__double_as_longlong(r) & 0xFFFFFFFFFFFFFull;
     }
-};
 
-// First-level bin of an entry: 1/16 binade of its weight, the last one
-// holding everything from 32 binades down.  fp32 is enough: the map only has
-// to be the same everywhere and not to rise with the value.
-__device__ __forceinline__ int coarse_bin(float v, float top, float c16)
-{
-    return v == top ? 0 : (int)fminf((top - v) * c16, (float)(kBins - 1));
-}
+    __device__ __forceinline__ u64 operator()(float v) const
+    {
+        double d;
+        const double m = scaled(v, d);
+        return weight(m, d);
+    }
+};
 
 // ------------------------------------------------------------ shared memory
 struct Hist {
@@ -135,24 +181,23 @@ struct Hist {
 };
 
 struct Shared {
-    double table[256];
-    Hist hist[3];
+    double table[64];
+    // [0], [1]: masses and counts of the first level; then [2] and [3], [0]
+    // and [1] in turn
+    Hist hist[4];
+    uint32_t list[kListCap];     // keys of the border bin
     u64 wmass[kMaxWarps];        // kept mass above the cut, per warp segment
     uint32_t wtie[kMaxWarps];    // entries equal to the cut, per warp segment
-    uint32_t list[kListCap];     // keys of the border bin
     u64 scan[kMaxWarps];
     uint32_t red[kMaxWarps];
     // exchanged with the peers
     uint32_t top_key, first;     // largest key; first index of the maximum
-    uint32_t kmin, kmax;         // keys in the border bin
+    u64 mass;                    // kept mass above the cut
+    uint32_t ties;               // entries equal to the cut
     // answers of a search
     int bin;
-    u64 base;
+    u64 base, total;
     int listed;
-    u64 total;
-    int owner;
-    u64 owner_base;
-    uint32_t owner_tie;
 };
 
 __device__ __forceinline__ u64 warp_sum(u64 v)
@@ -175,23 +220,19 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane)
 }
 
 // Adds w to a bin of this CTA's histogram (all lanes of the warp; w = 0: an
-// entry that does not count).  Integer sums: their order does not matter.
-// The low words carry into the high ones.  A warp whose entries fall into one
-// bin (rows of few distinct values) adds them up first: 32 atomics on one
-// word run one after another.
+// entry that does not count).  Integer sums: their order does not matter; the
+// low words carry into the high ones (a 64-bit shared-memory atomic is a
+// compare-and-swap loop, 43 cycles a warp against 9 for the two).  A warp
+// whose entries fall into one bin (rows of few distinct values) adds them up
+// first: 32 atomics on one word run one after another.
 template <bool MASS>
 __device__ __forceinline__ void hist_add(Hist &h, int bin, u64 w, int lane)
 {
-    const unsigned live = __ballot_sync(0xffffffffu, w != 0);
-    if (!live)
-        return;
-    const int b0 = __shfl_sync(0xffffffffu, bin, __ffs(live) - 1);
-    if (__all_sync(0xffffffffu, w == 0 || bin == b0)) {
-        const u64 s = MASS ? warp_sum(w) : (u64)__popc(live);
+    const int b0 = __shfl_sync(0xffffffffu, bin, 0);
+    if (__all_sync(0xffffffffu, bin == b0)) {
+        w = MASS ? warp_sum(w) : (u64)__popc(__ballot_sync(0xffffffffu, w != 0));
         if (lane != 0)
             return;
-        w = s;
-        bin = b0;
     }
     if (w == 0)
         return;
@@ -223,9 +264,17 @@ __device__ __forceinline__ void hist_find(Shared &s, const Hist &h, u64 base, u6
     const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
     const uint32_t n = cluster_size();
     u64 v = 0;
-    if (i < kBins)
-        for (uint32_t c = 0; c < n; ++c)
-            v += (u64)ld_peer(&h.lo[i], c) + ((u64)ld_peer(&h.hi[i], c) << 32);
+    if (i < kBins) {
+        uint32_t lo[kMaxCluster], hi[kMaxCluster];
+#pragma unroll
+        for (uint32_t c = 0; c < kMaxCluster; ++c) {
+            lo[c] = c < n ? ld_peer(&h.lo[i], c) : 0;
+            hi[c] = c < n ? ld_peer(&h.hi[i], c) : 0;
+        }
+#pragma unroll
+        for (uint32_t c = 0; c < kMaxCluster; ++c)
+            v += (u64)lo[c] + ((u64)hi[c] << 32);
+    }
     u64 incl = warp_scan(v, lane);
     if (lane == 31 && warp < kBins / 32)
         s.scan[warp] = incl;
@@ -251,6 +300,22 @@ __device__ __forceinline__ void hist_find(Shared &s, const Hist &h, u64 base, u6
     __syncthreads();
 }
 
+// Largest key in [lo, hi] for which `yes` holds, given that it holds for lo
+// and for no key above one for which it does not; 32 keys at a time.
+template <typename F>
+__device__ __forceinline__ uint32_t last_key(uint32_t lo, uint32_t hi, int lane, F yes)
+{
+    while (lo < hi) {
+        const uint32_t step = (hi - lo + 31) / 32;
+        const uint32_t k = lo + step * (lane + 1);
+        const bool in = k >= lo && k <= hi;   // no overflow
+        const int n = __popc(__ballot_sync(0xffffffffu, in && yes(k)));
+        lo += step * n;
+        hi = min(hi, lo + (step - 1));
+    }
+    return lo;
+}
+
 // ------------------------------------------------------------------- kernel
 template <typename T>
 __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
@@ -263,30 +328,42 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
     const int row = blockIdx.x / ncta;
     const int lo = min((int)rank * p.per, p.V);            // this CTA's entries
     const int cnt = min(lo + p.per, p.V) - lo;
-    for (int i = tid; i < 256; i += blockDim.x)
-        s.table[i] = exp2((double)i * (1.0 / 256.0));
-    for (int i = 0; i < 3; ++i)
+    const T *src = static_cast<const T *>(p.logits) + row * p.ld + lo;
+    // slots at the source's address modulo 16 bytes; a segment of whole 128
+    // slots per warp, in index order
+    constexpr int kVec = 16 / sizeof(T);
+    const int skew = (int)(reinterpret_cast<uintptr_t>(src) & 15u) / (int)sizeof(T);
+    const int seg = (skew + cnt + 128 * nwarps - 1) / (128 * nwarps) * 128;
+    const int used = (skew + cnt + 127) / 128 * 128;       // slots that any warp reads
+    const int b0 = min(used, warp * seg), b1 = min(used, b0 + seg);
+    T *data = reinterpret_cast<T *>(dyn);
+    for (int i = tid; i < 64; i += blockDim.x)
+        s.table[i] = exp2((double)i * (1.0 / 64.0));
+    for (int i = 0; i < 4; ++i)
         hist_clear(s.hist[i]);
     if (tid == 0) {
         s.first = 0xFFFFFFFFu;
-        s.kmin = 0xFFFFFFFFu;
-        s.kmax = 0;
         s.listed = 0;
     }
+    if (tid < skew)
+        data[tid] = bits_of<T>(-INFINITY);
+    for (int i = skew + cnt + tid; i < used; i += blockDim.x)
+        data[i] = bits_of<T>(-INFINITY);
     pdl_wait();
     pdl_launch_dependents();
+    const float temp = p.temperature ? __ldg(p.temperature + row) : 1.f;
+    const float top_p = p.top_p ? __ldg(p.top_p + row) : 1.f;
+    const float min_p = p.min_p ? __ldg(p.min_p + row) : 0.f;
+    const int top_k = p.top_k ? __ldg(p.top_k + row) : 0;
+    const float u = __ldg(p.u + row);
 
-    // ---- copy the slice, at its address modulo 16, and find the maximum
-    const T *src = static_cast<const T *>(p.logits) + row * p.ld + lo;
-    const int skew = (int)(reinterpret_cast<uintptr_t>(src) & 15u) / (int)sizeof(T);
-    T *data = reinterpret_cast<T *>(dyn) + skew;
+    // ---- copy the entries and find the maximum
     float mx = -INFINITY;
     {
-        constexpr int kVec = 16 / sizeof(T);
         const int head = min(cnt, (kVec - skew) % kVec);
         const int vecs = (cnt - head) / kVec;
         const uint4 *vsrc = reinterpret_cast<const uint4 *>(src + head);
-        uint4 *vdst = reinterpret_cast<uint4 *>(data + head);
+        uint4 *vdst = reinterpret_cast<uint4 *>(data + skew + head);
         for (int i0 = tid; i0 < vecs; i0 += 4 * blockDim.x) {
             uint4 v[4];
 #pragma unroll
@@ -296,23 +373,28 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (i0 + j * (int)blockDim.x < vecs) {
-                    vdst[i0 + j * blockDim.x] = v[j];
-                    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                    uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (sizeof(T) == 2) {
-                            mx = fmaxf(mx, fmaxf(value_of((uint16_t)w[k]),
-                                                 value_of((uint16_t)(w[k] >> 16))));
+                            const float a = canonical(__uint_as_float(w[k] << 16));
+                            const float b = canonical(__uint_as_float(w[k] & 0xFFFF0000u));
+                            mx = fmaxf(mx, fmaxf(a, b));
+                            w[k] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
                         } else {
-                            mx = fmaxf(mx, value_of((uint32_t)w[k]));
+                            const float a = canonical(__uint_as_float(w[k]));
+                            mx = fmaxf(mx, a);
+                            w[k] = __float_as_uint(a);
                         }
                     }
+                    vdst[i0 + j * blockDim.x] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
         }
         if (tid < cnt - vecs * kVec) {   // what the vectors leave: fewer than 2 kVec entries
             const int i = tid < head ? tid : tid + vecs * kVec;
-            data[i] = src[i];
-            mx = fmaxf(mx, value_of(data[i]));
+            const float a = canonical(value_of(src[i]));
+            data[skew + i] = bits_of<T>(a);
+            mx = fmaxf(mx, a);
         }
     }
     uint32_t mk = __reduce_max_sync(0xffffffffu, key_of(mx, (uint32_t)0));
@@ -325,83 +407,94 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
             s.top_key = mk;
     }
     cluster_barrier();
-    for (uint32_t c = 0; c < ncta; ++c)
-        mk = max(mk, ld_peer(&s.top_key, c));
-    mk = __reduce_max_sync(0xffffffffu, mk);
-    const float top = key_value(mk, (uint32_t)0);
-
-    const float temp = p.temperature ? __ldg(p.temperature + row) : 1.f;
-    // this warp's entries, in index order
-    const int seg = (((cnt + nwarps - 1) / nwarps) + 31) / 32 * 32;
-    const int b0 = min(cnt, warp * seg), b1 = min(cnt, b0 + seg);
+    mk = __reduce_max_sync(0xffffffffu, lane < (int)ncta ? ld_peer(&s.top_key, lane) : 0u);
+    float top = key_value(mk, (uint32_t)0);
 
     if (top == -INFINITY || !(temp > 0.f)) {   // nothing to take, or greedy
         if (top > -INFINITY)
-            for (int i = b0 + lane; i < b1; i += 32)
-                if (value_of(data[i]) == top) {
-                    atomicMin(&s.first, (uint32_t)(lo + i));
+            for (int i = b0 + 4 * lane; i < b1; i += 128) {
+                float v[4];
+                load4(data, i, v);
+                if (v[0] == top || v[1] == top || v[2] == top || v[3] == top) {
+                    const int e = v[0] == top ? 0 : v[1] == top ? 1 : v[2] == top ? 2 : 3;
+                    atomicMin(&s.first, (uint32_t)(lo + i + e - skew));
                     break;
                 }
+            }
         cluster_barrier();
-        if (rank == 0 && tid == 0) {
-            uint32_t first = s.first;
-            for (uint32_t c = 1; c < ncta; ++c)
-                first = min(first, ld_peer(&s.first, c));
-            p.tokens[row] = (int)first;
-            if (p.probs)
-                p.probs[row] = top > -INFINITY ? 1.f : 0.f;
+        if (rank == 0 && warp == 0) {
+            const uint32_t first = __reduce_min_sync(
+                0xffffffffu, lane < (int)ncta ? ld_peer(&s.first, lane) : 0xFFFFFFFFu);
+            if (lane == 0) {
+                p.tokens[row] = (int)first;
+                if (p.probs)
+                    p.probs[row] = top > -INFINITY ? 1.f : 0.f;
+            }
         }
         cluster_barrier();
         return;
     }
+    if (top == INFINITY) {
+        // the +inf entries share the mass: as zeros among -inf (every warp
+        // reads its own segment only)
+        for (int i = b0 + lane; i < b1; i += 32)
+            data[i] = bits_of<T>(value_of(data[i]) == INFINITY ? 0.f : -INFINITY);
+        __syncwarp();
+        top = 0.f;
+    }
 
     const double kLog2e = 1.4426950408889634074;
     Weights weight;
-    weight.top = top;
-    weight.dtop = (double)top;
-    weight.c = 256.0 * kLog2e / (double)temp;
+    weight.top = (double)top;
     weight.table = s.table;
-    const float c16 = (float)(16.0 * kLog2e / (double)temp);
+    {
+        // a temperature at which the next lower float has no weight is as
+        // good as any below it, and keeps (v - top) / T in range
+        const double gap = (double)top - (double)nextafterf(top, -INFINITY);
+        const double t = fmax((double)temp, gap * (kLog2e / 48.0));
+        weight.c = 64.0 * kLog2e / t;
+        weight.least = fmaxf(__double2float_rd((double)top - 48.0 / kLog2e * t), -FLT_MAX);
+    }
 
     // ---- min-p: the lowest value that passes (the test rises with the value)
     float low = -FLT_MAX;   // -inf never passes
-    const float min_p = p.min_p ? __ldg(p.min_p + row) : 0.f;
-    if (min_p > 0.f && top < INFINITY) {
+    if (min_p > 0.f) {
         const double cut = (double)temp * log(fmin((double)min_p, 1.0));
-        const double dtop = weight.dtop;
-        low = fmaxf(__double2float_rd(dtop + cut), -FLT_MAX);
+        low = fmaxf(__double2float_rd(weight.top + cut), -FLT_MAX);
         for (int i = 0; i < 2 && low > -FLT_MAX; ++i) {
             const float below = nextafterf(low, -INFINITY);
-            if (below > -INFINITY && (double)below - dtop >= cut)
+            if ((double)below - weight.top >= cut)
                 low = below;
         }
-        for (int i = 0; i < 3 && !((double)low - dtop >= cut); ++i)
+        for (int i = 0; i < 3 && (double)low - weight.top < cut; ++i)
             low = nextafterf(low, INFINITY);
-        low += 0.f;   // no -0
     }
-    uint32_t low_key = key_of(low, T(0));   // of the value truncated to T
-    if (key_value(low_key, T(0)) < low)
-        ++low_key;
 
-    // ---- the cut of top-p and top-k
-    const float top_p = p.top_p ? __ldg(p.top_p + row) : 1.f;
-    const int top_k = p.top_k ? __ldg(p.top_k + row) : 0;
+    // ---- the cut of top-p and top-k: keep values above it, and the first
+    // cut_ties in index order of those equal to it
     const bool use_p = top_p < 1.f, use_k = top_k > 0;
-    uint32_t cut_key = 0;              // keep keys above it, and ...
-    u64 cut_ties = ~0ull;              // ... the first so many equal to it
+    float cut = -INFINITY;
+    u64 cut_ties = 0;
     if (use_p || use_k) {
-        for (int i = b0 + lane; i - lane < b1; i += 32) {
-            const float v = i < b1 ? value_of(data[i]) : -INFINITY;
-            const bool in = v > -INFINITY;
-            const int bin = in ? coarse_bin(v, top, c16) : 0;
-            if (use_p)
-                hist_add<true>(s.hist[0], bin, in ? weight(v) : 0ull, lane);
-            if (use_k)
-                hist_add<false>(s.hist[1], bin, in ? 1ull : 0ull, lane);
+        for (int i = b0 + 4 * lane; i < b1; i += 128) {
+            float v[4];
+            load4(data, i, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = v[e] > -INFINITY;
+                double d;
+                const double m = weight.scaled(v[e], d);
+                const int bin = weight.bin(m);
+                if (use_p)
+                    hist_add<true>(s.hist[0], bin, in ? weight.weight(m, d) : 0ull, lane);
+                if (use_k)
+                    hist_add<false>(s.hist[1], bin, in ? 1ull : 0ull, lane);
+            }
         }
         cluster_barrier();
         int bin_p = kBins, bin_k = kBins;
         u64 base_p = 0, base_k = 0, target_p = 0;
+        const u64 target_k = (u64)max(top_k, 0);
         if (use_p) {
             hist_find(s, s.hist[0], 0, 0, (double)top_p);
             bin_p = s.bin;
@@ -410,7 +503,7 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
             __syncthreads();
         }
         if (use_k) {
-            hist_find(s, s.hist[1], 0, (u64)top_k, 0.0);
+            hist_find(s, s.hist[1], 0, target_k, 0.0);
             if (s.bin >= 0) {   // else the row has no more than top_k entries
                 bin_k = s.bin;
                 base_k = s.base;
@@ -421,105 +514,119 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
         // fall into one bin
         const int bin = min(bin_p, bin_k);
         if (bin < kBins) {
-            // list the keys of that bin (or, when they are too many, look
-            // through the slice again each time)
-            uint32_t least = 0xFFFFFFFFu, most = 0;
-            for (int i = b0 + lane; i - lane < b1; i += 32) {
-                const float v = i < b1 ? value_of(data[i]) : -INFINITY;
-                const uint32_t k = key_of(v, T(0));
-                const bool in = v > -INFINITY && coarse_bin(v, top, c16) == bin;
-                const unsigned found = __ballot_sync(0xffffffffu, in);
-                if (!found)
-                    continue;
-                int at = 0;
-                if (lane == 0)
-                    at = atomicAdd(&s.listed, __popc(found));
-                at = __shfl_sync(0xffffffffu, at, 0) + __popc(found & ((1u << lane) - 1));
-                if (in) {
-                    if (at < kListCap)
-                        s.list[at] = k;
-                    least = min(least, k);
-                    most = max(most, k);
+            const bool do_p = bin_p == bin, do_k = bin_k == bin;
+            // the bin's keys are kl .. kh
+            const uint32_t k_min = key_of(-FLT_MAX, T(0)), k_top = key_of(top, T(0));
+            auto key_bin = [&](uint32_t k) { return weight.bin(key_value(k, T(0))); };
+            const uint32_t kh = bin == 0 ? k_top
+                                         : last_key(k_min, k_top, lane,
+                                                    [&](uint32_t k) { return key_bin(k) >= bin; });
+            uint32_t kl = k_min;
+            if (key_bin(k_min) > bin)
+                kl = last_key(k_min, kh, lane, [&](uint32_t k) { return key_bin(k) > bin; }) + 1;
+            const float vl = key_value(kl, T(0)), vh = key_value(kh, T(0));
+            const int sh0 = max(0, 32 - __clz(kh - kl) - 9);   // bins of 2^sh keys from kh down
+            // second level: a histogram of those keys, and a list of them for
+            // the levels behind it (when they are too many for the list, those
+            // look through the slots again)
+            for (int i = b0 + 4 * lane; i < b1; i += 128) {
+                float v[4];
+                load4(data, i, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool in = v[e] >= vl && v[e] <= vh;
+                    const unsigned found = __ballot_sync(0xffffffffu, in);
+                    if (!found)
+                        continue;
+                    const uint32_t k = key_of(v[e], T(0));
+                    const int b = in ? (int)((kh - k) >> sh0) : 0;
+                    if (do_p)
+                        hist_add<true>(s.hist[2], b, in ? weight(v[e]) : 0ull, lane);
+                    if (do_k)
+                        hist_add<false>(s.hist[3], b, in ? 1ull : 0ull, lane);
+                    if (sh0 > 0) {
+                        int at = 0;
+                        if (lane == 0)
+                            at = atomicAdd(&s.listed, __popc(found));
+                        at = __shfl_sync(0xffffffffu, at, 0) + __popc(found & ((1u << lane) - 1));
+                        if (in && at < kListCap)
+                            s.list[at] = k;
+                    }
                 }
-            }
-            least = __reduce_min_sync(0xffffffffu, least);
-            most = __reduce_max_sync(0xffffffffu, most);
-            if (lane == 0 && least <= most) {
-                atomicMin(&s.kmin, least);
-                atomicMax(&s.kmax, most);
             }
             cluster_barrier();
-            uint32_t kmin = 0xFFFFFFFFu, kmax = 0;
-            for (uint32_t c = 0; c < ncta; ++c) {
-                kmin = min(kmin, ld_peer(&s.kmin, c));
-                kmax = max(kmax, ld_peer(&s.kmax, c));
-            }
             const bool listed = s.listed <= kListCap;
-            const int entries = listed ? s.listed : cnt;
-            int level = 0;
+            const int entries = listed ? s.listed : used;
+            hist_clear(s.hist[0]);   // the peers have read these by now
+            hist_clear(s.hist[1]);
+            // the histogram of a further level: masses ([2] or [0]) or counts ([3] or [1])
             auto refine = [&](auto mass, u64 base, u64 target, uint32_t &key, u64 &ties) {
                 constexpr bool MASS = decltype(mass)::value;
-                uint32_t kl = kmin, kh = kmax;
-                while (kl < kh) {
-                    const uint32_t range = kh - kl;   // bins of 2^sh keys from kh down
-                    const int sh = max(0, 32 - __clz(range) - 9);
-                    Hist &h = s.hist[level & 1 ? 0 : 2];
+                Hist *h = MASS ? &s.hist[2] : &s.hist[3], *other = MASS ? &s.hist[0] : &s.hist[1];
+                uint32_t l = kl, r = kh;
+                int sh = sh0;
+                while (true) {
+                    hist_find(s, *h, base, target, 0.0);
+                    base = s.base;
+                    r -= (uint32_t)s.bin << sh;
+                    l = max(l, r - ((1u << sh) - 1));
+                    if (sh == 0)
+                        break;
+                    __syncthreads();
+                    Hist *t = h;
+                    h = other;
+                    other = t;
+                    sh = l < r ? max(0, 32 - __clz(r - l) - 9) : 0;
                     for (int i = tid; i - lane < entries; i += blockDim.x) {
                         uint32_t k = 0;
-                        bool in = i < entries;
-                        if (in && listed) {
-                            k = s.list[i];
-                        } else if (in) {
-                            const float v = value_of(data[i]);
-                            in = v > -INFINITY;
-                            k = key_of(v, T(0));
-                        }
-                        in = in && k >= kl && k <= kh;
+                        if (i < entries)
+                            k = listed ? s.list[i] : key_of(value_of(data[i]), T(0));
+                        const bool in = k >= l && k <= r;
                         const u64 w = !in ? 0ull : MASS ? weight(key_value(k, T(0))) : 1ull;
-                        hist_add<MASS>(h, in ? (int)((kh - k) >> sh) : 0, w, lane);
+                        hist_add<MASS>(*h, in ? (int)((r - k) >> sh) : 0, w, lane);
                     }
                     cluster_barrier();
-                    // the peers have read the other histogram by now
-                    hist_clear(s.hist[level & 1 ? 2 : 0]);
-                    hist_find(s, h, base, target, 0.0);
-                    const uint32_t b = (uint32_t)s.bin;
-                    base = s.base;
-                    kh -= b << sh;
-                    kl = max(kl, kh - ((1u << sh) - 1));
-                    ++level;
-                    __syncthreads();
+                    hist_clear(*other);   // read by the peers before this barrier
                 }
-                key = kh;
-                const u64 each = MASS ? weight(key_value(kh, T(0))) : 1ull;
+                __syncthreads();
+                key = r;
+                const u64 each = MASS ? weight(key_value(r, T(0))) : 1ull;
                 ties = (target - base + each - 1) / each;
             };
-            uint32_t key = 0;
+            uint32_t key = 0, cut_key = 0;
             u64 ties = 0;
-            if (bin_p == bin) {
+            if (do_p) {
                 refine(std::true_type(), base_p, target_p, key, ties);
                 cut_key = key;
                 cut_ties = ties;
             }
-            if (bin_k == bin) {
-                refine(std::false_type(), base_k, (u64)top_k, key, ties);
+            if (do_k) {
+                refine(std::false_type(), base_k, target_k, key, ties);
                 if (key > cut_key || (key == cut_key && ties < cut_ties)) {
                     cut_key = key;
                     cut_ties = ties;
                 }
             }
+            cut = key_value(cut_key, T(0));
         }
     }
 
-    // ---- kept mass per warp segment, in index order
+    // ---- kept mass per warp segment and CTA
+    const float keep = fmaxf(low, cut);    // what is kept is at least this ...
+    const bool tied = cut >= low;          // ... and above the cut or among the first ties
     u64 mass = 0;
     uint32_t tie = 0;
-    for (int i = b0 + lane; i < b1; i += 32) {
-        const float v = value_of(data[i]);
-        const uint32_t k = key_of(v, T(0));
-        if (k >= low_key && k > cut_key)
-            mass += weight(v);
-        else if (k >= low_key && k == cut_key)
-            ++tie;
+    for (int i = b0 + 4 * lane; i < b1; i += 128) {
+        float v[4];
+        load4(data, i, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (v[e] >= keep) {
+                if (v[e] == cut)
+                    ++tie;
+                else
+                    mass += weight(v[e]);
+            }
     }
     mass = warp_sum(mass);
     tie = __reduce_add_sync(0xffffffffu, tie);
@@ -527,73 +634,90 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
         s.wmass[warp] = mass;
         s.wtie[warp] = tie;
     }
+    __syncthreads();
+    if (warp == 0) {
+        const u64 m = warp_sum(lane < nwarps ? s.wmass[lane] : 0ull);
+        const uint32_t n = __reduce_add_sync(0xffffffffu, lane < nwarps ? s.wtie[lane] : 0u);
+        if (lane == 0) {
+            s.mass = m;
+            s.ties = n;
+        }
+    }
     cluster_barrier();
-    // every CTA adds all segments: thread i takes segment i of the row
-    const u64 each = cut_key ? weight(key_value(cut_key, T(0))) : 0;
-    {
-        const int n = (int)ncta * nwarps;   // at most 256, below blockDim
-        u64 m = 0;
-        u64 ti = 0;
-        if (tid < n) {
-            m = ld_peer64(&s.wmass[tid % nwarps], tid / nwarps);
-            ti = ld_peer(&s.wtie[tid % nwarps], tid / nwarps);
-        }
-        // ties before each segment, then the mass each keeps
-        u64 t_incl = warp_scan(ti, lane);
-        if (lane == 31)
-            s.scan[warp] = t_incl;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w)
-            t_incl += s.scan[w];
-        const u64 before = t_incl - ti;
-        const u64 kept_ties = before >= cut_ties ? 0 : min(ti, cut_ties - before);
-        m += kept_ties * each;
-        u64 incl = warp_scan(m, lane);
-        __syncthreads();
-        if (lane == 31)
-            s.scan[warp] = incl;
-        __syncthreads();
-        u64 total = 0;
-        for (int w = 0; w < nwarps; ++w) {
-            if (w < warp)
-                incl += s.scan[w];
-            total += s.scan[w];
-        }
-        // first entry whose running sum exceeds u * total (u >= 1 or NaN:
-        // the last one with a weight)
-        const double x = (double)__ldg(p.u + row) * (double)total;
-        u64 target = total - 1;
-        if (x < (double)target)
-            target = x > 0.0 ? (u64)x : 0;
-        if (tid < n && incl > target && incl - m <= target) {
-            s.owner = tid;
-            s.owner_base = incl - m;
-            s.owner_tie = (uint32_t)min(before, (u64)0xFFFFFFFFu);
-            s.total = target;
-        }
-        __syncthreads();
-        const int owner = s.owner;
-        if ((int)rank == owner / nwarps && warp == owner % nwarps) {
-            u64 run = s.owner_base;
-            uint32_t ties = s.owner_tie;
-            const u64 want = s.total;
-            for (int i = b0 + lane; i - lane < b1; i += 32) {
+    // ---- where u * (kept mass) falls: the CTA, then its warp (every warp
+    // works that out for itself), then the entry.  of() gives each lane the
+    // kept mass of its part from the mass above the cut and the ties in it
+    const u64 each = tied ? weight(cut) : 0ull;
+    auto of = [&](u64 m, u64 n, u64 &before) {
+        before += warp_scan(n, lane) - n;
+        return m + each * (before >= cut_ties ? 0ull : min(n, cut_ties - before));
+    };
+    u64 ties_before = 0;
+    u64 part = 0, n = 0;
+    if (lane < (int)ncta) {
+        part = ld_peer64(&s.mass, lane);
+        n = ld_peer(&s.ties, lane);
+    }
+    // the peers' shared memory is not read after this point
+    cluster_arrive();
+    part = of(part, n, ties_before);
+    u64 incl = warp_scan(part, lane);
+    const u64 total = __shfl_sync(0xffffffffu, incl, 31);
+    // the entry whose running sum first exceeds u * total (u >= 1 or NaN:
+    // the last one with a weight)
+    const double x = (double)u * (double)total;
+    u64 target = total - 1;
+    if (x < (double)target)
+        target = x > 0.0 ? (u64)x : 0;
+    int at = __ffs(__ballot_sync(0xffffffffu, incl > target)) - 1;
+    if (at == (int)rank) {
+        u64 before = __shfl_sync(0xffffffffu, incl - part, at);
+        ties_before = __shfl_sync(0xffffffffu, ties_before, at);
+        part = of(lane < nwarps ? s.wmass[lane] : 0ull, lane < nwarps ? s.wtie[lane] : 0u,
+                  ties_before);
+        incl = before + warp_scan(part, lane);
+        at = __ffs(__ballot_sync(0xffffffffu, incl > target)) - 1;
+        if (at == warp) {
+            before = __shfl_sync(0xffffffffu, incl - part, at);
+            ties_before = __shfl_sync(0xffffffffu, ties_before, at);
+            // a 32nd of the segment per lane, then its entries
+            const int sub = seg / 32;   // a multiple of 4
+            mass = 0;
+            tie = 0;
+            for (int i = b0 + lane * sub; i < min(b1, b0 + (lane + 1) * sub); i += 4) {
+                float v[4];
+                load4(data, i, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (v[e] >= keep) {
+                        if (v[e] == cut)
+                            ++tie;
+                        else
+                            mass += weight(v[e]);
+                    }
+            }
+            __syncwarp();
+            part = of(mass, tie, ties_before);
+            incl = before + warp_scan(part, lane);
+            at = __ffs(__ballot_sync(0xffffffffu, incl > target)) - 1;
+            u64 run = __shfl_sync(0xffffffffu, incl - part, at);
+            ties_before = __shfl_sync(0xffffffffu, ties_before, at);
+            const int e0 = b0 + at * sub, e1 = min(b1, e0 + sub);
+            for (int i = e0 + lane; i - lane < e1; i += 32) {
+                const float v = i < e1 ? value_of(data[i]) : -INFINITY;
+                const bool in = v >= keep;
+                const unsigned equal = __ballot_sync(0xffffffffu, in && v == cut);
                 u64 w = 0;
-                const float v = i < b1 ? value_of(data[i]) : -INFINITY;
-                const uint32_t k = key_of(v, T(0));
-                const bool in = i < b1 && k >= low_key;
-                const unsigned equal = __ballot_sync(0xffffffffu, in && k == cut_key);
-                if (in && k > cut_key)
+                if (in && v != cut)
                     w = weight(v);
-                else if (in && k == cut_key &&
-                         ties + __popc(equal & ((1u << lane) - 1)) < cut_ties)
+                else if (in && ties_before + __popc(equal & ((1u << lane) - 1)) < cut_ties)
                     w = each;
-                ties += __popc(equal);
+                ties_before += __popc(equal);
                 const u64 sum = run + warp_scan(w, lane);
-                const unsigned hit = __ballot_sync(0xffffffffu, sum > want);
+                const unsigned hit = __ballot_sync(0xffffffffu, sum > target);
                 if (hit) {
                     if (lane == __ffs(hit) - 1) {
-                        p.tokens[row] = lo + i;
+                        p.tokens[row] = lo + i - skew;
                         if (p.probs)
                             p.probs[row] = (float)((double)w / (double)total);
                     }
@@ -603,7 +727,7 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
             }
         }
     }
-    cluster_barrier();   // the peers have read this CTA's shared memory
+    cluster_wait();
 }
 
 template <typename T>
@@ -619,7 +743,7 @@ cudaError_t launch_typed(const SamplePlan &pl, const SampleParams &p, cudaStream
     static std::atomic<bool> done[kMaxDeviceCache];
     if (!done[dev].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmemSlice + 32);
+                                 kSmemSlice + kSlack * (int)sizeof(T));
         if (e != cudaSuccess)
             return e;
         done[dev].store(true, std::memory_order_release);
@@ -652,7 +776,7 @@ SamplePlan plan_sample(int device, int M, int V, bool fp32)
         pl.cluster *= 2;
     pl.per = ((V + pl.cluster - 1) / pl.cluster + 7) / 8 * 8;
     pl.threads = (long long)M * pl.cluster <= sms ? 1024 : 512;
-    pl.smem = (size_t)pl.per * size + 32;
+    pl.smem = ((size_t)pl.per + kSlack) * size;   // whole groups of 128 slots, and the skew
     return pl;
 }
 
