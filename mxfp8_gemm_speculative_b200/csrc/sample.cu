@@ -40,6 +40,7 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kBins = 512;
+constexpr int kGroups = 32;       // of 16 bins, a lane each
 constexpr int kListCap = 2048;    // entries of the border bin a CTA lists
 constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = 32;
@@ -178,26 +179,31 @@ struct Weights {
 // ------------------------------------------------------------ shared memory
 struct Hist {
     uint32_t lo[kBins], hi[kBins];   // 64-bit sums in two words
+    u64 group[kGroups];              // sums of kBins / kGroups bins
+};
+
+// A search for a border: the bins of the next histogram are the 2^sh keys
+// each from r down to l, and `base` lies above them.
+struct Search {
+    u64 target, base;
+    uint32_t l, r;
+    int sh;
+    int bin;      // first level: the border's bin, kBins without a border
 };
 
 struct Shared {
     double table[64];
-    // [0], [1]: masses and counts of the first level; then [2] and [3], [0]
-    // and [1] in turn
-    Hist hist[4];
+    Hist hist[2][2];             // [level parity][masses, counts]
+    Search find[2];              // top-p (masses), top-k (counts)
     uint32_t list[kListCap];     // keys of the border bin
     u64 wmass[kMaxWarps];        // kept mass above the cut, per warp segment
     uint32_t wtie[kMaxWarps];    // entries equal to the cut, per warp segment
-    u64 scan[kMaxWarps];
     uint32_t red[kMaxWarps];
+    int listed;
     // exchanged with the peers
     uint32_t top_key, first;     // largest key; first index of the maximum
     u64 mass;                    // kept mass above the cut
     uint32_t ties;               // entries equal to the cut
-    // answers of a search
-    int bin;
-    u64 base, total;
-    int listed;
 };
 
 __device__ __forceinline__ u64 warp_sum(u64 v)
@@ -219,32 +225,22 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane)
     return v;
 }
 
-// Adds w to a bin of this CTA's histogram (all lanes of the warp; w = 0: an
-// entry that does not count).  Integer sums: their order does not matter; the
-// low words carry into the high ones (a 64-bit shared-memory atomic is a
-// compare-and-swap loop, 43 cycles a warp against 9 for the two).  A warp
-// whose entries fall into one bin (rows of few distinct values) adds them up
-// first: 32 atomics on one word run one after another.
+// Adds w to a bin of this CTA's histogram.  Integer sums: their order does not
+// matter; the low words carry into the high ones (a 64-bit shared-memory
+// atomic is a compare-and-swap loop, 43 cycles a warp against 9 for the two).
 template <bool MASS>
-__device__ __forceinline__ void hist_add(Hist &h, int bin, u64 w, int lane)
+__device__ __forceinline__ void hist_add(Hist &h, int bin, u64 w)
 {
-    const int b0 = __shfl_sync(0xffffffffu, bin, 0);
-    if (__all_sync(0xffffffffu, bin == b0)) {
-        w = MASS ? warp_sum(w) : (u64)__popc(__ballot_sync(0xffffffffu, w != 0));
-        if (lane != 0)
-            return;
-    }
-    if (w == 0)
-        return;
-    if (!MASS) {
-        atomicAdd(&h.lo[bin], (uint32_t)w);
-        return;
-    }
     const uint32_t lo = (uint32_t)w;
-    const uint32_t old = atomicAdd(&h.lo[bin], lo);
-    const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
-    if (hi)
-        atomicAdd(&h.hi[bin], hi);
+    if (!MASS) {
+        if (lo)
+            atomicAdd(&h.lo[bin], lo);
+    } else if (w) {
+        const uint32_t old = atomicAdd(&h.lo[bin], lo);
+        const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
+        if (hi)
+            atomicAdd(&h.hi[bin], hi);
+    }
 }
 
 __device__ __forceinline__ void hist_clear(Hist &h)
@@ -255,49 +251,67 @@ __device__ __forceinline__ void hist_clear(Hist &h)
     }
 }
 
-// The border in the cluster's histogram h (complete in every CTA): s.bin is
-// the first bin whose running sum, from `base`, reaches the target, s.base
-// the sum before it, s.total the sum of all bins; s.bin = -1 when no bin
-// reaches it.  target = 0: ceil(p * total), at least 1.
-__device__ __forceinline__ void hist_find(Shared &s, const Hist &h, u64 base, u64 target, double p)
+// The sums of this CTA's groups of bins, from a complete histogram: a thread
+// per group of 16, one after another (few bins, off no critical path wider
+// than a barrier).
+__device__ __forceinline__ void hist_groups(Hist &h, int thread)
 {
-    const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
-    const uint32_t n = cluster_size();
-    u64 v = 0;
-    if (i < kBins) {
-        uint32_t lo[kMaxCluster], hi[kMaxCluster];
+    if (thread >= 0 && thread < kGroups) {
+        u64 v = 0;
 #pragma unroll
-        for (uint32_t c = 0; c < kMaxCluster; ++c) {
-            lo[c] = c < n ? ld_peer(&h.lo[i], c) : 0;
-            hi[c] = c < n ? ld_peer(&h.hi[i], c) : 0;
+        for (int j = 0; j < kBins / kGroups; ++j) {
+            // each thread starts at another bank
+            const int i = thread * (kBins / kGroups) + ((j + thread) & (kBins / kGroups - 1));
+            v += (u64)h.lo[i] + ((u64)h.hi[i] << 32);
         }
-#pragma unroll
-        for (uint32_t c = 0; c < kMaxCluster; ++c)
-            v += (u64)lo[c] + ((u64)hi[c] << 32);
+        h.group[thread] = v;
     }
-    u64 incl = warp_scan(v, lane);
-    if (lane == 31 && warp < kBins / 32)
-        s.scan[warp] = incl;
-    if (i == 0)
-        s.bin = -1;
-    __syncthreads();
-    u64 total = 0;
+}
+
+// The border in the cluster's histogram h, by one warp: the first bin whose
+// running sum from `base` reaches the target, with the sum before it in base;
+// kBins when none does.  target = 0: ceil(p * (sum of all bins)), at least 1.
+// Reads the peers' groups first, then the bins of one group: a quarter of a
+// kilobyte per peer and not the four of the whole histogram.
+__device__ __forceinline__ int hist_find(const Hist &h, u64 &base, u64 &target, double p, int lane)
+{
+    const uint32_t n = cluster_size();
+    u64 part[kMaxCluster], v = 0;
 #pragma unroll
-    for (int w = 0; w < kBins / 32; ++w) {
-        if (w < warp)
-            incl += s.scan[w];
-        total += s.scan[w];
-    }
+    for (uint32_t c = 0; c < kMaxCluster; ++c)
+        part[c] = c < n ? ld_peer64(&h.group[lane], c) : 0;
+#pragma unroll
+    for (uint32_t c = 0; c < kMaxCluster; ++c)
+        v += part[c];
+    u64 incl = base + warp_scan(v, lane);
     if (target == 0)
-        target = max(1ull, (u64)ceil(p * (double)total));
-    incl += base;
-    if (i < kBins && incl >= target && incl - v < target) {
-        s.bin = i;
-        s.base = incl - v;
+        target = max(1ull, (u64)ceil(p * (double)(__shfl_sync(0xffffffffu, incl, 31) - base)));
+    const unsigned over = __ballot_sync(0xffffffffu, incl >= target);
+    if (!over)
+        return kBins;
+    const int g = __ffs(over) - 1;
+    base = __shfl_sync(0xffffffffu, incl - v, g);
+    // 16 bins, the peers shared between the halves of the warp
+    constexpr int kPer = kBins / kGroups;
+    const int i = g * kPer + lane % kPer;
+    uint32_t lo[kMaxCluster / 2], hi[kMaxCluster / 2];
+#pragma unroll
+    for (uint32_t c = 0; c < kMaxCluster / 2; ++c) {
+        const uint32_t peer = 2 * c + lane / kPer;
+        lo[c] = peer < n ? ld_peer(&h.lo[i], peer) : 0;
+        hi[c] = peer < n ? ld_peer(&h.hi[i], peer) : 0;
     }
-    if (i == 0)
-        s.total = total;
-    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (uint32_t c = 0; c < kMaxCluster / 2; ++c)
+        v += (u64)lo[c] + ((u64)hi[c] << 32);
+    v += __shfl_xor_sync(0xffffffffu, v, kPer);
+    if (lane >= kPer)
+        v = 0;
+    incl = base + warp_scan(v, lane);
+    const int b = __ffs(__ballot_sync(0xffffffffu, incl >= target)) - 1;
+    base = __shfl_sync(0xffffffffu, incl - v, b);
+    return g * kPer + b;
 }
 
 // Largest key in [lo, hi] for which `yes` holds, given that it holds for lo
@@ -340,7 +354,7 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
     for (int i = tid; i < 64; i += blockDim.x)
         s.table[i] = exp2((double)i * (1.0 / 64.0));
     for (int i = 0; i < 4; ++i)
-        hist_clear(s.hist[i]);
+        hist_clear(s.hist[i / 2][i % 2]);
     if (tid == 0) {
         s.first = 0xFFFFFFFFu;
         s.listed = 0;
@@ -476,45 +490,83 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
     float cut = -INFINITY;
     u64 cut_ties = 0;
     if (use_p || use_k) {
-        for (int i = b0 + 4 * lane; i < b1; i += 128) {
-            float v[4];
-            load4(data, i, v);
+        // first level: all entries, four a lane and step
+        auto first_level = [&](auto with_p, auto with_k) {
+            constexpr bool P = decltype(with_p)::value, K = decltype(with_k)::value;
+            for (int i = b0 + 4 * lane; i < b1; i += 128) {
+                float v[4];
+                load4(data, i, v);
+                u64 w[4] = {};
+                int bin[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool in = v[e] > -INFINITY;
-                double d;
-                const double m = weight.scaled(v[e], d);
-                const int bin = weight.bin(m);
-                if (use_p)
-                    hist_add<true>(s.hist[0], bin, in ? weight.weight(m, d) : 0ull, lane);
-                if (use_k)
-                    hist_add<false>(s.hist[1], bin, in ? 1ull : 0ull, lane);
+                for (int e = 0; e < 4; ++e) {
+                    double d;
+                    const double m = weight.scaled(v[e], d);
+                    bin[e] = weight.bin(m);
+                    if (P)
+                        w[e] = v[e] > -INFINITY ? weight.weight(m, d) : 0;
+                }
+                // a warp whose entries fall into one bin (rows of equal
+                // values) adds them up first: 32 atomics on one word run one
+                // after another
+                const bool one = bin[0] == __shfl_sync(0xffffffffu, bin[0], 0) &&
+                                 bin[1] == bin[0] && bin[2] == bin[0] && bin[3] == bin[0];
+                if (__all_sync(0xffffffffu, one)) {
+                    const u64 sum = P ? warp_sum(w[0] + w[1] + w[2] + w[3]) : 0;
+                    uint32_t n = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        n += v[e] > -INFINITY;
+                    n = K ? __reduce_add_sync(0xffffffffu, n) : 0;
+                    if (lane == 0) {
+                        if (P)
+                            hist_add<true>(s.hist[0][0], bin[0], sum);
+                        if (K)
+                            hist_add<false>(s.hist[0][1], bin[0], n);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (P)
+                            hist_add<true>(s.hist[0][0], bin[e], w[e]);
+                        if (K)
+                            hist_add<false>(s.hist[0][1], bin[e], v[e] > -INFINITY);
+                    }
+                }
             }
-        }
-        cluster_barrier();
-        int bin_p = kBins, bin_k = kBins;
-        u64 base_p = 0, base_k = 0, target_p = 0;
-        const u64 target_k = (u64)max(top_k, 0);
-        if (use_p) {
-            hist_find(s, s.hist[0], 0, 0, (double)top_p);
-            bin_p = s.bin;
-            base_p = s.base;
-            target_p = max(1ull, (u64)ceil((double)top_p * (double)s.total));
+        };
+        if (use_p && use_k)
+            first_level(std::true_type(), std::true_type());
+        else if (use_p)
+            first_level(std::true_type(), std::false_type());
+        else
+            first_level(std::false_type(), std::true_type());
+        // completes this level's histograms in the cluster
+        int level = 0;
+        auto exchange = [&](bool do_p, bool do_k) {
             __syncthreads();
+            if (do_p)
+                hist_groups(s.hist[level & 1][0], tid);
+            if (do_k)
+                hist_groups(s.hist[level & 1][1], tid - 64);
+            cluster_barrier();
+        };
+        exchange(use_p, use_k);
+        // warp 0 looks for top-p's border, warp 1 for top-k's
+        if (warp < 2) {
+            u64 base = 0, target = warp ? (u64)max(top_k, 0) : 0;
+            int bin = kBins;   // no border: the filter is off, or keeps all
+            if (warp ? use_k : use_p)
+                bin = hist_find(s.hist[0][warp], base, target, (double)top_p, lane);
+            if (lane == 0)
+                s.find[warp] = Search{target, base, 0, 0, 0, bin};
         }
-        if (use_k) {
-            hist_find(s, s.hist[1], 0, target_k, 0.0);
-            if (s.bin >= 0) {   // else the row has no more than top_k entries
-                bin_k = s.bin;
-                base_k = s.base;
-            }
-            __syncthreads();
-        }
+        __syncthreads();
         // the stricter filter decides; both are followed when their borders
         // fall into one bin
-        const int bin = min(bin_p, bin_k);
+        const int bin = min(s.find[0].bin, s.find[1].bin);
         if (bin < kBins) {
-            const bool do_p = bin_p == bin, do_k = bin_k == bin;
+            const bool do_p = s.find[0].bin == bin, do_k = s.find[1].bin == bin;
             // the bin's keys are kl .. kh
             const uint32_t k_min = key_of(-FLT_MAX, T(0)), k_top = key_of(top, T(0));
             auto key_bin = [&](uint32_t k) { return weight.bin(key_value(k, T(0))); };
@@ -526,82 +578,100 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
                 kl = last_key(k_min, kh, lane, [&](uint32_t k) { return key_bin(k) > bin; }) + 1;
             const float vl = key_value(kl, T(0)), vh = key_value(kh, T(0));
             const int sh0 = max(0, 32 - __clz(kh - kl) - 9);   // bins of 2^sh keys from kh down
-            // second level: a histogram of those keys, and a list of them for
+            __syncthreads();
+            if (tid < 2) {
+                s.find[tid].l = kl;
+                s.find[tid].r = kh;
+                s.find[tid].sh = sh0;
+            }
+            // second level: histograms of those keys, and a list of them for
             // the levels behind it (when they are too many for the list, those
             // look through the slots again)
             for (int i = b0 + 4 * lane; i < b1; i += 128) {
                 float v[4];
                 load4(data, i, v);
+                bool in[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    in[e] = v[e] >= vl && v[e] <= vh;
+                if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3]))
+                    continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const bool in = v[e] >= vl && v[e] <= vh;
-                    const unsigned found = __ballot_sync(0xffffffffu, in);
+                    const unsigned found = __ballot_sync(0xffffffffu, in[e]);
                     if (!found)
                         continue;
                     const uint32_t k = key_of(v[e], T(0));
-                    const int b = in ? (int)((kh - k) >> sh0) : 0;
+                    const int b = in[e] ? (int)((kh - k) >> sh0) : 0;
+                    u64 w = in[e] && do_p ? weight(v[e]) : 0;
+                    uint32_t n = in[e];
+                    const int f = __ffs(found) - 1;
+                    const int bf = __shfl_sync(0xffffffffu, b, f);
+                    if (__all_sync(0xffffffffu, !in[e] || b == bf)) {   // as above
+                        w = do_p ? warp_sum(w) : 0;
+                        n = __popc(found);
+                        if (lane != f)
+                            w = n = 0;
+                    }
                     if (do_p)
-                        hist_add<true>(s.hist[2], b, in ? weight(v[e]) : 0ull, lane);
+                        hist_add<true>(s.hist[1][0], b, w);
                     if (do_k)
-                        hist_add<false>(s.hist[3], b, in ? 1ull : 0ull, lane);
+                        hist_add<false>(s.hist[1][1], b, n);
                     if (sh0 > 0) {
                         int at = 0;
                         if (lane == 0)
                             at = atomicAdd(&s.listed, __popc(found));
                         at = __shfl_sync(0xffffffffu, at, 0) + __popc(found & ((1u << lane) - 1));
-                        if (in && at < kListCap)
+                        if (in[e] && at < kListCap)
                             s.list[at] = k;
                     }
                 }
             }
-            cluster_barrier();
-            const bool listed = s.listed <= kListCap;
-            const int entries = listed ? s.listed : used;
-            hist_clear(s.hist[0]);   // the peers have read these by now
-            hist_clear(s.hist[1]);
-            // the histogram of a further level: masses ([2] or [0]) or counts ([3] or [1])
-            auto refine = [&](auto mass, u64 base, u64 target, uint32_t &key, u64 &ties) {
-                constexpr bool MASS = decltype(mass)::value;
-                Hist *h = MASS ? &s.hist[2] : &s.hist[3], *other = MASS ? &s.hist[0] : &s.hist[1];
-                uint32_t l = kl, r = kh;
-                int sh = sh0;
-                while (true) {
-                    hist_find(s, *h, base, target, 0.0);
-                    base = s.base;
-                    r -= (uint32_t)s.bin << sh;
-                    l = max(l, r - ((1u << sh) - 1));
-                    if (sh == 0)
-                        break;
-                    __syncthreads();
-                    Hist *t = h;
-                    h = other;
-                    other = t;
-                    sh = l < r ? max(0, 32 - __clz(r - l) - 9) : 0;
-                    for (int i = tid; i - lane < entries; i += blockDim.x) {
-                        uint32_t k = 0;
-                        if (i < entries)
-                            k = listed ? s.list[i] : key_of(value_of(data[i]), T(0));
-                        const bool in = k >= l && k <= r;
-                        const u64 w = !in ? 0ull : MASS ? weight(key_value(k, T(0))) : 1ull;
-                        hist_add<MASS>(*h, in ? (int)((r - k) >> sh) : 0, w, lane);
-                    }
-                    cluster_barrier();
-                    hist_clear(*other);   // read by the peers before this barrier
+            // further levels, until both searches are at one key
+            bool open = true;
+            while (open) {
+                level ^= 1;
+                exchange(do_p, do_k);
+                hist_clear(s.hist[level ^ 1][0]);   // the peers have read these by now
+                hist_clear(s.hist[level ^ 1][1]);
+                if (warp < 2 && (warp ? do_k : do_p) && s.find[warp].sh >= 0) {
+                    Search f = s.find[warp];
+                    const int b = hist_find(s.hist[level][warp], f.base, f.target, 0.0, lane);
+                    f.r -= (uint32_t)b << f.sh;
+                    f.l = max(f.l, f.r - ((1u << f.sh) - 1));
+                    // the next bins, or -1: l = r is the border
+                    f.sh = f.l < f.r ? max(0, 32 - __clz(f.r - f.l) - 9) : -1;
+                    __syncwarp();
+                    if (lane == 0)
+                        s.find[warp] = f;
                 }
                 __syncthreads();
-                key = r;
-                const u64 each = MASS ? weight(key_value(r, T(0))) : 1ull;
-                ties = (target - base + each - 1) / each;
-            };
-            uint32_t key = 0, cut_key = 0;
-            u64 ties = 0;
+                const Search fp = s.find[0], fk = s.find[1];
+                const bool more_p = do_p && fp.sh >= 0, more_k = do_k && fk.sh >= 0;
+                open = more_p || more_k;
+                if (!open)
+                    break;
+                const bool listed = s.listed <= kListCap;
+                const int entries = listed ? s.listed : used;
+                for (int i = tid; i < entries; i += blockDim.x) {
+                    const uint32_t k = listed ? s.list[i] : key_of(value_of(data[i]), T(0));
+                    if (more_p && k >= fp.l && k <= fp.r)
+                        hist_add<true>(s.hist[level ^ 1][0], (int)((fp.r - k) >> fp.sh),
+                                       weight(key_value(k, T(0))));
+                    if (more_k && k >= fk.l && k <= fk.r)
+                        hist_add<false>(s.hist[level ^ 1][1], (int)((fk.r - k) >> fk.sh), 1ull);
+                }
+            }
+            // the stricter cut of the two
+            uint32_t cut_key = 0;
             if (do_p) {
-                refine(std::true_type(), base_p, target_p, key, ties);
-                cut_key = key;
-                cut_ties = ties;
+                cut_key = s.find[0].r;
+                const u64 each = weight(key_value(cut_key, T(0)));
+                cut_ties = (s.find[0].target - s.find[0].base + each - 1) / each;
             }
             if (do_k) {
-                refine(std::false_type(), base_k, target_k, key, ties);
+                const u64 ties = s.find[1].target - s.find[1].base;
+                const uint32_t key = s.find[1].r;
                 if (key > cut_key || (key == cut_key && ties < cut_ties)) {
                     cut_key = key;
                     cut_ties = ties;
