@@ -372,10 +372,11 @@ MXG_API int bf16_gemm_small_ex(const void *X, const void *W, int M, int N, int K
  *           range of a fused projection's output will do.  Out may be Y
  *           itself (then ldo = ldy), which this call exempts from the
  *           no-alias rule; otherwise the two must not overlap;
- *   workspace  device, lora_workspace_bytes(M, N, K, R) bytes for the inner
- *           products X * A^T; needs no initialisation and keeps nothing that
- *           a later call reads.  Not the workspace of a call that may run at
- *           the same time.
+ *   workspace  device, lora_workspace_bytes(M, N, K, R) bytes: a status word
+ *           (mxg_workspace_status; each call clears it) and the inner products
+ *           X * A^T.  Needs no initialisation and keeps nothing that a later
+ *           call reads.  Not the workspace of a call that may run at the same
+ *           time, nor one that a GEMM uses (those keep their counters in it).
  * The inner products are held to 16 bits of mantissa at least (not rounded to
  * bf16), sums in fp32; Out is rounded once.  Bitwise reproducible.  Unlike the
  * GEMMs, nothing is read before the previous kernel on `stream` has

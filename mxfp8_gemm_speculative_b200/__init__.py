@@ -16,6 +16,7 @@ grow it on demand; pass ``workspace=`` to manage it yourself.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -139,9 +140,14 @@ def _stream(stream=None, device=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def _on_device(device):
     """Makes ``device`` current for a C call: the library plans and launches
     on the current device (its SM count, its kernels, its static scratch)."""
+    if torch.cuda.current_device() == device.index:
+        return _HERE_ALREADY
     return torch.cuda.device(device)
 
 
@@ -696,18 +702,46 @@ def bf16_gemm_small(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None =
 
 
 # ------------------------------------------------------- low-rank adapters
+# Calls of a few microseconds: the checks below take the pointer of an
+# argument that is in order at once, and look for what is wrong only otherwise.
+def _dense(t: torch.Tensor, dtype, shape, device, name: str) -> int:
+    """The pointer of a contiguous tensor of this type and shape."""
+    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        _need_shape(t, shape, name)
+        _same_device(t, device, name)
+        _need(t, dtype, name)
+    return t.data_ptr()
+
+
+def _need_cuda(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _empty_as(t: torch.Tensor, dtype, stream) -> torch.Tensor:
+    """_empty of a contiguous tensor's shape (half the host time)."""
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, dtype=dtype)
+
+
 def _need_rows(t: torch.Tensor, M: int, N: int, device, name: str) -> int:
     """The row stride of a bf16 [M][N] whose rows are contiguous."""
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != N:
+    if t.shape != (M, N):
         raise ValueError(f"{name} must be [{M}][{N}], got {list(t.shape)}")
-    _same_device(t, device, name)
-    if N > 1 and t.stride(1) != 1:
+    if t.device != device:
+        _same_device(t, device, name)
+    ld, one = t.stride()
+    if one != 1 and N > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     if M == 1:
         return -(-N // 8) * 8      # one row: its stride says nothing
-    return t.stride(0)
+    return ld
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor, lda: int, ldb: int) -> bool:
@@ -727,34 +761,28 @@ def _overlap(a: torch.Tensor, b: torch.Tensor, lda: int, ldb: int) -> bool:
 def _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream):
     """The arguments of the C call, and the tensors behind them."""
     dev = x.device
+    _need_cuda(x, "x")
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a must be [L][R][K] and b [L][N][R]")
     L, R, K = a.shape
     N = b.shape[1]
-    if b.shape[0] != L or b.shape[2] != R:
-        raise ValueError(f"b must be [{L}][N][{R}], got {list(b.shape)}")
     if x.dim() != 2:
         raise ValueError(f"x must be [M][{K}], got {list(x.shape)}")
     M = x.shape[0]
-    _need(a, torch.bfloat16, "a")
-    _need(b, torch.bfloat16, "b")
-    _need(index, torch.int32, "index")
-    if index.dim() != 1 or index.shape[0] != M:
-        raise ValueError(f"index must be [{M}], got {list(index.shape)}")
+    pa = _dense(a, torch.bfloat16, (L, R, K), dev, "a")
+    pb = _dense(b, torch.bfloat16, (L, N, R), dev, "b")
+    pi = _dense(index, torch.int32, (M,), dev, "index")
+    ps = None if scales is None else _dense(scales, torch.float32, (L,), dev, "scales")
     ldx = _need_rows(x, M, K, dev, "x")
     ldy = _need_rows(y, M, N, dev, "y")
-    for t, name in ((a, "a"), (b, "b"), (index, "index")):
-        _same_device(t, dev, name)
-    if scales is not None:
-        _need(scales, torch.float32, "scales")
-        if scales.dim() != 1 or scales.shape[0] != L:
-            raise ValueError(f"scales must be [{L}], got {list(scales.shape)}")
-        _same_device(scales, dev, "scales")
-    need = lora_workspace_bytes(M, N, K, R)
+    need = _lora_bytes(M, N, K, R)
     if need == 0:
         raise MxgError(MXG_ERR_UNSUPPORTED_SHAPE, "lora_add")
     if out is None:
-        out = _empty((M, N), torch.bfloat16, dev, stream)
+        if y.is_contiguous():
+            out = _empty_as(y, torch.bfloat16, stream)
+        else:
+            out = _empty((M, N), torch.bfloat16, dev, stream)
         ldo = N
     else:
         ldo = _need_rows(out, M, N, dev, "out")
@@ -764,17 +792,23 @@ def _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream):
     if workspace_buf is None:
         # this call's own, from the stream's pool: calls captured into
         # different graphs never share it
-        ws = _empty(need, torch.uint8, dev, stream)
+        if stream is None:
+            ws = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev)
+        else:
+            ws = _empty((need,), torch.uint8, dev, stream)
     else:
         ws = workspace_buf
         _need_ws(ws, dev)
-    args = (_ptr(x), ldx, _ptr(a), _ptr(b), _ptr(scales), _ptr(index), _ptr(y), ldy, _ptr(out),
-            ldo, M, N, K, R, L, _ptr(ws), ws.numel())
+    args = (x.data_ptr(), ldx, pa, pb, ps, pi, y.data_ptr(), ldy, out.data_ptr(), ldo, M, N, K, R,
+            L, ws.data_ptr(), ws.numel())
     return args, out, (x, a, b, scales, index, y, out, ws, stream)
 
 
 def lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
     return int(_lib.lora_workspace_bytes(M, N, K, R))
+
+
+_lora_bytes = functools.lru_cache(maxsize=4096)(lora_workspace_bytes)   # of the sizes alone
 
 
 def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor,
@@ -806,34 +840,36 @@ def prepare_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: t
 def _sample_args(logits, u, temperature, top_k, top_p, min_p, tokens, probs, stream):
     """The arguments of the C call, its outputs, and the tensors behind them."""
     dev = logits.device
+    _need_cuda(logits, "logits")
     if logits.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [M][V], got {list(logits.shape)}")
     M, V = logits.shape
-    if V > 1 and logits.stride(1) != 1:
+    ld, one = logits.stride()
+    if one != 1 and V > 1:
         raise ValueError("the rows of logits must be contiguous")
-    ld = logits.stride(0) if M > 1 else V
+    if M == 1:
+        ld = V
     if u is None:
         raise ValueError("u must be given: one random number per row")
-    given = ((u, torch.float32, "u"), (temperature, torch.float32, "temperature"),
-             (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"),
-             (min_p, torch.float32, "min_p"), (tokens, torch.int32, "tokens"),
-             (probs, torch.float32, "probs"))
-    for t, dtype, name in given:
-        if t is None:
-            continue
-        _need(t, dtype, name)
-        if t.dim() != 1 or t.shape[0] != M:
-            raise ValueError(f"{name} must be [{M}], got {list(t.shape)}")
-        _same_device(t, dev, name)
+    shape = (M,)
+    f32, i32 = torch.float32, torch.int32
+    pu = _dense(u, f32, shape, dev, "u")
+    pt = None if temperature is None else _dense(temperature, f32, shape, dev, "temperature")
+    pk = None if top_k is None else _dense(top_k, i32, shape, dev, "top_k")
+    pp = None if top_p is None else _dense(top_p, f32, shape, dev, "top_p")
+    pq = None if min_p is None else _dense(min_p, f32, shape, dev, "min_p")
     if tokens is None:
-        tokens = _empty((M,), torch.int32, dev, stream)
+        tokens = _empty_as(u, i32, stream)
+    else:
+        _dense(tokens, i32, shape, dev, "tokens")
     if probs is None:
-        probs = _empty((M,), torch.float32, dev, stream)
-    args = (_ptr(logits), DTYPE_BF16 if logits.dtype == torch.bfloat16 else DTYPE_FP32, ld, M, V,
-            _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens),
-            _ptr(probs))
+        probs = _empty_as(u, f32, stream)
+    else:
+        _dense(probs, f32, shape, dev, "probs")
+    args = (logits.data_ptr(), DTYPE_BF16 if logits.dtype == torch.bfloat16 else DTYPE_FP32, ld, M,
+            V, pu, pt, pk, pp, pq, tokens.data_ptr(), probs.data_ptr())
     return args, (tokens, probs), (logits, u, temperature, top_k, top_p, min_p, tokens, probs,
                                    stream)
 

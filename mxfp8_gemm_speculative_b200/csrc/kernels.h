@@ -113,8 +113,9 @@ struct LoraPlan {
     int slices;           // rank slices of that many tiles
     int cluster;          // CTAs that split K (shrink)
     int shrink_subs, expand_subs;   // CTAs that share a block's groups
-    int expand_warps;     // warps (of 32 columns) per expand CTA
-    int ntiles;           // column tiles (expand)
+    int expand_steps;     // 16-rank steps of the expand variant (1, 2, 4, 8)
+    int expand_shares;    // CTAs that share the tokens of a column tile
+    int ntiles;           // column tiles of 256 (expand)
 };
 struct LoraArgs {
     const void *X, *A, *B, *Y;
@@ -126,7 +127,7 @@ struct LoraArgs {
     void *workspace;
 };
 bool lora_shape_ok(int M, int N, int K, int R);
-size_t lora_scratch_bytes(int M, int R);   // the [M][R] inner products
+size_t lora_scratch_bytes(int M, int R);   // status header and the [M][R] inner products
 LoraPlan plan_lora(int device, int M, int N, int K, int R);   // of a shape that is ok
 cudaError_t launch_lora(const LoraPlan &plan, const LoraArgs &args, cudaStream_t stream);
 

@@ -19,10 +19,10 @@
 //   expand   Out = Y + T B^T, summed in fp32 and rounded once.
 //
 // Tokens come in any order.  Both kernels take blocks of 64 consecutive
-// tokens and group a block's tokens by adapter in shared memory (a few
-// hundred cycles; no sort kernel, no host plan, nothing read back), so an
-// adapter is read once per block that uses it and once in all for a decode
-// batch.
+// tokens, and every warp groups a block's tokens by adapter for itself with
+// match and ballot instructions (no sort kernel, no host plan, nothing read
+// back, no barrier), so an adapter is read once per block that uses it and
+// once in all for a decode batch.
 #include <algorithm>
 #include <atomic>
 
@@ -32,89 +32,98 @@
 namespace mxg {
 namespace {
 
+typedef unsigned long long u64;
+
 constexpr int kBlockTok = 64;     // tokens grouped together
-constexpr int kShrinkWarps = 8;   // warps that split K in a shrink CTA
+constexpr int kShrinkWarps = 8;
+constexpr int kFew = 16;          // tokens of a group that takes the smaller stages
 
 struct LoraParams {
     const uint16_t *X, *A, *B, *Y;   // bf16
     uint16_t *Out;
     const float *scales;     // [L] or NULL (all 1)
     const int *index;        // [M]
+    WsHeader *hdr;           // status word, cleared by the shrink kernel
     uint4 *T;                // [M][R / 4]: four hi halves, then four lo halves
     long long ldx, ldy, ldo; // row strides in elements
     int M, N, K, R, L;
 };
 
-// 16-byte load that bypasses L1 (adapters are read once per CTA).
-__device__ __forceinline__ uint4 ldg128_once(const void *p)
+// 16 bytes global -> shared, asynchronous; zeros when `in` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in)
 {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // -------------------------------------------------------- tokens by adapter
+// The block's tokens grouped by adapter, in the registers of a warp: lane l
+// knows tokens l and l + 32, with the tokens (a bit each) of their groups.
 struct Groups {
-    int adapter[kBlockTok];          // per token of the block (-1: none)
-    int group[kBlockTok];            // its group, numbered by first token
-    int g_adapter[kBlockTok];        // per group
-    int g_begin[kBlockTok + 1];      // its tokens are list[g_begin .. next g_begin)
-    short list[kBlockTok];           // token offsets in the block, by group
-    unsigned leaders[2];             // bit per token: the first of its group
+    int a0, a1;        // adapters (-1: none, -2: no such token)
+    u64 of0, of1;      // tokens of the same adapter
+    u64 leaders;       // first token of every group
 };
 
-// Groups the block's `ntok` tokens; returns the number of groups.  Called by
-// every thread of a CTA of at least 64.
-__device__ __forceinline__ int group_tokens(Groups &s, const int *index, int ntok, int L)
+// raw0, raw1: the index of tokens lane and lane + 32 (anything behind ntok).
+__device__ __forceinline__ Groups group_tokens(int raw0, int raw1, int ntok, int L, int lane)
 {
-    const int i = threadIdx.x;
-    if (i < kBlockTok) {
-        const int a = i < ntok ? __ldcg(index + i) : -1;
-        s.adapter[i] = a >= 0 && a < L ? a : -1;
-    }
-    __syncthreads();
-    if (i < kBlockTok) {
-        const int a = s.adapter[i];
-        int first = i;
-        for (int j = ntok - 1; j >= 0; --j)
-            if (s.adapter[j] == a)
-                first = j;
-        s.group[i] = first;   // token that leads the group, renumbered below
-        const unsigned lead = __ballot_sync(0xffffffffu, i < ntok && first == i);
-        if ((i & 31) == 0)
-            s.leaders[i >> 5] = lead;
-    }
-    __syncthreads();
-    const unsigned lo = s.leaders[0], hi = s.leaders[1];
-    int grp = -1;
-    if (i < ntok) {
-        const int f = s.group[i];
-        grp = f < 32 ? __popc(lo & ((1u << f) - 1)) : __popc(lo) + __popc(hi & ((1u << (f - 32)) - 1));
-        if (f == i)
-            s.g_adapter[grp] = s.adapter[i];
-    }
-    __syncthreads();
-    if (i < ntok)
-        s.group[i] = grp;
-    __syncthreads();
-    if (i < ntok) {
-        int before = 0, rank = 0;   // tokens of earlier groups; earlier tokens of this one
-        for (int j = 0; j < ntok; ++j) {
-            const int gj = s.group[j];
-            before += gj < grp;
-            rank += gj == grp && j < i;
+    Groups g;
+    g.a0 = lane >= ntok ? -2 : raw0 >= 0 && raw0 < L ? raw0 : -1;
+    g.a1 = lane + 32 >= ntok ? -2 : raw1 >= 0 && raw1 < L ? raw1 : -1;
+    const unsigned m0 = __match_any_sync(0xffffffffu, g.a0);
+    const unsigned lead0 = __ballot_sync(0xffffffffu, g.a0 != -2 && __ffs(m0) - 1 == lane);
+    g.of0 = m0;
+    g.of1 = 0;
+    g.leaders = lead0;
+    if (ntok > 32) {
+        const unsigned m1 = __match_any_sync(0xffffffffu, g.a1);
+        g.of1 = (u64)m1 << 32;
+        // every adapter of the upper half: which tokens of the lower have it
+        unsigned lead1 = __ballot_sync(0xffffffffu, g.a1 != -2 && __ffs(m1) - 1 == lane);
+        for (unsigned rest = lead1; rest; rest &= rest - 1) {
+            const int l = __ffs(rest) - 1;
+            const int a = __shfl_sync(0xffffffffu, g.a1, l);
+            const unsigned upper = __shfl_sync(0xffffffffu, m1, l);
+            const unsigned lower = __ballot_sync(0xffffffffu, g.a0 == a);
+            if (g.a0 == a)
+                g.of0 |= (u64)upper << 32;
+            if (g.a1 == a)
+                g.of1 |= lower;
+            if (lower)
+                lead1 &= ~(1u << l);
         }
-        s.list[before + rank] = (short)i;
-        if (rank == 0)
-            s.g_begin[grp] = before;
+        g.leaders |= (u64)lead1 << 32;
     }
-    const int ngroups = __popc(lo) + __popc(hi);
-    if (i == 0)
-        s.g_begin[ngroups] = ntok;
-    __syncthreads();
-    return ngroups;
+    return g;
+}
+
+// The group that token `first` leads: its adapter, its number of tokens, and
+// those (offsets in the block, rising) in this warp's list.
+__device__ __forceinline__ int take_group(const Groups &g, int first, uint8_t *list, int lane,
+                                          int &adapter)
+{
+    const int l = first & 31;
+    const bool up = first >= 32;
+    adapter = __shfl_sync(0xffffffffu, up ? g.a1 : g.a0, l);
+    const u64 of = __shfl_sync(0xffffffffu, up ? g.of1 : g.of0, l);
+    __syncwarp();   // the list's last readers are done
+    if (of >> lane & 1)
+        list[__popcll(of & ((1ull << lane) - 1))] = (uint8_t)lane;
+    if (of >> (lane + 32) & 1)
+        list[__popcll(of & ((1ull << (lane + 32)) - 1))] = (uint8_t)(lane + 32);
+    __syncwarp();
+    return __popcll(of);
 }
 
 __device__ __forceinline__ float4 ld_peer_f4(const void *p, uint32_t rank)
@@ -136,280 +145,618 @@ __device__ __forceinline__ void split_bf16(float v, uint32_t &hi, uint32_t &lo)
     lo = (hi & 0x7F80u) == 0x7F80u ? 0u : f32_to_bf16_bits(rest);
 }
 
+// Two fp32 values rounded to a bf16 pair.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // ------------------------------------------------------------------- shrink
 // One cluster per (block of tokens, share of its groups, slice of 16 RT
-// ranks); its CTAs split K, and each CTA's warps split that again in units of
-// 32: a lane loads 16 bytes (eight k) per row, so the fragments of two
-// m16n8k16 MMAs (ranks as the 16 rows, tokens as the 8 columns) come straight
-// from global memory, X and A in the same k order.  Warps are added through
-// shared memory and CTAs through distributed shared memory in a fixed order
-// (bitwise reproducible; no atomics, no second pass over partial sums).
-// 8 NT tokens of one adapter run together, so A is read once for them.
-template <int RT, int NT>
+// ranks); its CTAs split K and are added through distributed shared memory in
+// rank order (bitwise reproducible; no atomics, no partial sums in memory).
+// A CTA streams its K range of a group's rows of X (gathered by token) and of
+// the adapter's rows of A through a ring of 64-k stages in shared memory,
+// filled by asynchronous copies.  MMAs have the ranks as their 16 rows and 8
+// tokens as their columns; a warp takes one 32-k half of every stage, and the
+// halves are added at the end.  A group of up to 16 tokens (decode and verify
+// chunks, where the bytes of A are what counts) takes smaller stages and more
+// of them: in flight is what covers the latency.  Neither that choice nor a
+// token's place in the batch changes the order of its sums.
+template <int RT>
+struct Shrink {
+    // stages of `rows` tokens: 64 k of each and of the ranks
+    static constexpr int stage(int rows) { return (rows + 16 * RT) * 128; }
+    static constexpr int kManyStages = 5, kFewStages = RT == 1 ? 12 : 8;
+    static constexpr int kMany = kManyStages * stage(kBlockTok), kFewRing = kFewStages * stage(kFew);
+    static constexpr int kRing = kMany > kFewRing ? kMany : kFewRing;
+    static constexpr int ST = 16 * RT + 4;                 // row stride of the reduced tile
+    static constexpr int kTile = kBlockTok * ST * (int)sizeof(float);
+    static_assert(kTile <= kRing, "the second halves go into the ring");
+    static constexpr size_t smem = (size_t)kRing + kTile;
+};
+
+// The inner products of `ntok` <= ROWS tokens (offsets from x in `list`) with
+// the ranks of a slice (`ranks` rows of `arow`) over k0 .. k1, into
+// tile[token][rank].
+template <int RT, int ROWS, int STAGES>
+__device__ __forceinline__ void shrink_group(const LoraParams &p, const uint16_t *x,
+                                             const uint8_t *list, int ntok, const uint16_t *arow,
+                                             int ranks, int k0, int k1, uint8_t *ring, float *tile)
+{
+    using C = Shrink<RT>;
+    constexpr int kStage = C::stage(ROWS), kXStage = ROWS * 128;
+    constexpr int kTiles = ROWS / 8;                              // of 8 tokens
+    constexpr int kPer = (kTiles + kShrinkWarps / 2 - 1) / (kShrinkWarps / 2);   // per warp
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int q = warp / (kShrinkWarps / 2), first = warp % (kShrinkWarps / 2);
+    // Stage rows of 128 bytes are eight chunks of 16; chunk c of row r lies at
+    // c ^ 4 (r & 1), so the two rows that eight lanes load together use all
+    // banks.  Rows of absent tokens and ranks are not filled: they only reach
+    // results that nobody reads.
+    const int chunk = tid & 7;
+    auto fill = [&](int k, int slot) {
+        const uint32_t st = smem_u32(ring) + slot * kStage;
+        const int kc = k + 8 * chunk;
+        const bool in = kc < k1;
+        for (int r = tid >> 3; r < ROWS + 16 * RT; r += kShrinkWarps * 4) {
+            const uint16_t *src;
+            if (r < ROWS) {
+                if (r >= ntok)
+                    continue;
+                src = x + list[r] * p.ldx;
+            } else {
+                if (r - ROWS >= ranks)
+                    continue;
+                src = arow + (size_t)(r - ROWS) * p.K;
+            }
+            cp_async16(st + r * 128 + ((chunk ^ (r & 1) << 2) << 4), src + (in ? kc : 0), in);
+        }
+    };
+    float acc[kPer][RT][4];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[j][i][e] = 0.f;
+    const int steps = (k1 - k0 + 63) / 64;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+        if (s < steps)
+            fill(k0 + 64 * s, s);
+        cp_async_commit();
+    }
+    int slot = 0, next = STAGES - 1;
+    for (int s = 0; s < steps; ++s) {
+        cp_async_wait<STAGES - 2>();
+        __syncthreads();   // stage s is complete, stage s - 1 has been read
+        if (s + STAGES - 1 < steps)
+            fill(k0 + 64 * (s + STAGES - 1), next);
+        cp_async_commit();
+        if (8 * first < ntok) {
+            const uint32_t c = ((4 * q + t) ^ (g & 1) << 2) << 4;
+            const uint32_t st = smem_u32(ring) + slot * kStage + g * 128 + c;
+            uint4 xv[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                xv[j] = lds128a(st + 8 * (first + j * (kShrinkWarps / 2)) * 128);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const uint4 a0 = lds128a(st + kXStage + 16 * i * 128);
+                const uint4 a1 = lds128a(st + kXStage + (16 * i + 8) * 128);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    mma_bf16_16816(acc[j][i], a0.x, a1.x, a0.y, a1.y, xv[j].x, xv[j].y);
+                    mma_bf16_16816(acc[j][i], a0.z, a1.z, a0.w, a1.w, xv[j].z, xv[j].w);
+                }
+            }
+        }
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        next = next + 1 == STAGES ? 0 : next + 1;
+    }
+    // the second halves go through the ring, once it has been read, to the first
+    cp_async_wait<0>();
+    __syncthreads();
+    constexpr int ST = C::ST;
+    float *other = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int pass = 1; pass >= 0; --pass) {
+        if (q == pass)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int c = 8 * (first + j * (kShrinkWarps / 2)) + 2 * t;
+                if (c - 2 * t < min(ntok, ROWS))
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = (c + (e & 1)) * ST + 16 * i + g + 8 * (e >> 1);
+                            if (pass)
+                                other[at] = acc[j][i][e];
+                            else
+                                tile[at] = acc[j][i][e] + other[at];
+                        }
+            }
+        if (pass)
+            __syncthreads();
+    }
+}
+
+template <int RT>
 __global__ void __launch_bounds__(kShrinkWarps * 32, 2) lora_shrink_kernel(const LoraParams p)
 {
-    constexpr int CT = 8 * NT;        // tokens per chunk
-    constexpr int ST = 16 * RT + 4;   // row stride of the reduced tile (floats)
-    __shared__ Groups grp;
-    extern __shared__ float4 red[];   // [warps][RT * NT][32], then the CTA's tile
-    float *tile = reinterpret_cast<float *>(red + kShrinkWarps * RT * NT * 32);   // [CT][ST]
+    using C = Shrink<RT>;
+    constexpr int ST = C::ST;
+    __shared__ uint8_t lists[kShrinkWarps][kBlockTok];
+    extern __shared__ __align__(128) uint8_t dyn[];
+    float *tile = reinterpret_cast<float *>(dyn + C::kRing);   // [tokens][ST]
 
     // The dependent launch is allowed only after this wait: the expand kernel
     // may then read the index, B and Y before its own wait, since everything
     // queued before this kernel has completed.
     pdl_wait();
     pdl_launch_dependents();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+        p.hdr->status = p.hdr->where = 0;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nslices = (p.R + 16 * RT - 1) / (16 * RT);
     const int block = blockIdx.z / nslices, slice = blockIdx.z % nslices;
-    const int m0 = block * kBlockTok;
-    const int ngroups = group_tokens(grp, p.index + m0, min(kBlockTok, p.M - m0), p.L);
+    const int m0 = block * kBlockTok, r0 = slice * 16 * RT;
+    const Groups grp = group_tokens(m0 + lane < p.M ? __ldcg(p.index + m0 + lane) : -1,
+                                    m0 + lane + 32 < p.M ? __ldcg(p.index + m0 + lane + 32) : -1,
+                                    min(kBlockTok, p.M - m0), p.L, lane);
+    uint8_t *list = lists[warp];
     const int crank = (int)cluster_rank(), csize = (int)cluster_size();
-    const int units = (p.K + 31) / 32;
-    const int u0 = (int)((long long)crank * units / csize);
-    const int u1 = (int)((long long)(crank + 1) * units / csize);
-    const int r0 = slice * 16 * RT;
+    const int units = (p.K + 63) / 64;
+    const int k0 = (int)((long long)crank * units / csize) * 64;
+    const int k1 = min(p.K, (int)((long long)(crank + 1) * units / csize) * 64);
 
-    int n = 0;   // chunks seen so far: this cluster takes every gridDim.y-th
-    for (int gi = 0; gi < ngroups; ++gi) {
-        const int a = grp.g_adapter[gi];
+    int n = 0;   // groups seen so far: this cluster takes every gridDim.y-th
+    for (u64 rest = grp.leaders; rest; rest &= rest - 1) {
+        int a;
+        if (n % (int)gridDim.y != (int)blockIdx.y) {
+            const int first = __ffsll(rest) - 1;
+            a = __shfl_sync(0xffffffffu, first >= 32 ? grp.a1 : grp.a0, first & 31);
+            n += a >= 0;
+            continue;
+        }
+        const int ntok = take_group(grp, __ffsll(rest) - 1, list, lane, a);
         if (a < 0)
             continue;
-        const int end = grp.g_begin[gi + 1];
-        for (int begin = grp.g_begin[gi]; begin < end; begin += CT, ++n) {
-            if (n % gridDim.y != blockIdx.y)
-                continue;
-            const int ntok = min(CT, end - begin);
-            const int nt_live = (ntok + 7) / 8;
-            float acc[RT][NT][4];
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] = 0.f;
-            // this lane's rows: ranks g and g + 8 of every rank tile, token
-            // g of every token tile (absent ones stay zero)
-            const uint16_t *xrow[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int slot = 8 * j + g;
-                xrow[j] = slot < ntok ? p.X + (m0 + grp.list[begin + slot]) * p.ldx : nullptr;
+        ++n;
+        const uint16_t *x = p.X + m0 * p.ldx;
+        const uint16_t *arow = p.A + ((size_t)a * p.R + r0) * p.K;
+        const int ranks = min(16 * RT, p.R - r0);
+        if (ntok <= kFew)
+            shrink_group<RT, kFew, C::kFewStages>(p, x, list, ntok, arow, ranks, k0, k1, dyn, tile);
+        else
+            shrink_group<RT, kBlockTok, C::kManyStages>(p, x, list, ntok, arow, ranks, k0, k1, dyn,
+                                                        tile);
+        cluster_barrier();
+        // ---- add the CTAs of the cluster in rank order: every CTA finishes a
+        // share of the (token, four ranks) entries
+        const int quads = ranks / 4;
+        const float sc = p.scales ? __ldg(p.scales + a) : 1.f;
+        for (int e = tid * csize + crank; e < ntok * quads; e += kShrinkWarps * 32 * csize) {
+            const int c = e / quads, q = e % quads;
+            const float *mine = tile + c * ST + 4 * q;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < csize; ++w) {
+                const float4 v = ld_peer_f4(mine, w);
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
             }
-            const uint16_t *abase = p.A + (size_t)a * p.R * p.K + (size_t)(r0 + g) * p.K;
-#pragma unroll 2
-            for (int u = u0 + warp; u < u1; u += kShrinkWarps) {
-                const int k = 32 * u + 8 * t;
-                const bool in = k < p.K;
-                uint4 av[RT][2], xv[NT];
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        av[i][h] = make_uint4(0u, 0u, 0u, 0u);
-                        if (in && r0 + 16 * i + 8 * h + g < p.R)
-                            av[i][h] = ldg128_once(abase + (size_t)(16 * i + 8 * h) * p.K + k);
-                    }
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    xv[j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && xrow[j])
-                        xv[j] = ldg128(xrow[j] + k);
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    if (j < nt_live)
-#pragma unroll
-                        for (int i = 0; i < RT; ++i) {
-                            mma_bf16_16816(acc[i][j], av[i][0].x, av[i][1].x, av[i][0].y,
-                                           av[i][1].y, xv[j].x, xv[j].y);
-                            mma_bf16_16816(acc[i][j], av[i][0].z, av[i][1].z, av[i][0].w,
-                                           av[i][1].w, xv[j].z, xv[j].w);
-                        }
-            }
-            // ---- add the warps, in warp order
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    if (j < nt_live)
-                        red[((warp * NT + j) * RT + i) * 32 + lane] =
-                            make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-            __syncthreads();
-            for (int e = threadIdx.x; e < nt_live * RT * 32; e += kShrinkWarps * 32) {
-                float4 s = red[e];
-#pragma unroll
-                for (int w = 1; w < kShrinkWarps; ++w) {
-                    const float4 v = red[w * NT * RT * 32 + e];
-                    s.x += v.x;
-                    s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
-                }
-                const int l = e & 31, i = (e >> 5) % RT, j = (e >> 5) / RT;
-                const int r = 16 * i + (l >> 2), c = 8 * j + 2 * (l & 3);
-                tile[c * ST + r] = s.x;
-                tile[(c + 1) * ST + r] = s.y;
-                tile[c * ST + r + 8] = s.z;
-                tile[(c + 1) * ST + r + 8] = s.w;
-            }
-            cluster_barrier();
-            // ---- add the CTAs of the cluster in rank order: every CTA
-            // finishes a share of the (token, four ranks) entries
-            const int quads = min(16 * RT, p.R - r0) / 4;
-            const float sc = p.scales ? __ldg(p.scales + a) : 1.f;
-            for (int e = threadIdx.x * csize + crank; e < ntok * quads;
-                 e += kShrinkWarps * 32 * csize) {
-                const int c = e / quads, q = e % quads;
-                const float *mine = tile + c * ST + 4 * q;
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int w = 0; w < csize; ++w) {
-                    const float4 v = ld_peer_f4(mine, w);
-                    s.x += v.x;
-                    s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
-                }
-                uint32_t hi[4], lo[4];
-                split_bf16(s.x * sc, hi[0], lo[0]);
-                split_bf16(s.y * sc, hi[1], lo[1]);
-                split_bf16(s.z * sc, hi[2], lo[2]);
-                split_bf16(s.w * sc, hi[3], lo[3]);
-                p.T[(size_t)(m0 + grp.list[begin + c]) * (p.R / 4) + r0 / 4 + q] =
-                    make_uint4(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16),
-                               lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-            }
-            cluster_barrier();   // the tiles are read before the next chunk's
+            uint32_t hi[4], lo[4];
+            split_bf16(s.x * sc, hi[0], lo[0]);
+            split_bf16(s.y * sc, hi[1], lo[1]);
+            split_bf16(s.z * sc, hi[2], lo[2]);
+            split_bf16(s.w * sc, hi[3], lo[3]);
+            p.T[(size_t)(m0 + list[c]) * (p.R / 4) + r0 / 4 + q] =
+                make_uint4(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16), lo[0] | (lo[1] << 16),
+                           lo[2] | (lo[3] << 16));
         }
+        cluster_barrier();   // the tiles are read before the next group's
     }
 }
 
 // ------------------------------------------------------------------- expand
-// One warp per 32 columns and (block of tokens, share of its groups): the
-// rows of B for its columns stay in registers as MMA operands while the
-// group's tokens pass, 16 at a time (tokens as the 16 rows, columns as the 8
-// of four MMAs).  Column c of MMA i is column 8 (c / 2) + 2 i + c % 2 of the
-// warp's 32, so a lane's results are eight consecutive columns and Y and Out
-// move 16 bytes a lane, 64 contiguous bytes a row.  S = 16-rank steps.
+// A CTA takes 256 columns and a list of parts, up to 16 tokens of one adapter
+// each: those of a range of blocks, or (few blocks) of a share of one block's
+// groups.  Y, Out and T are bytes that are used once, B once per run of parts
+// of one adapter, so what counts is how many of them are in flight: a producer
+// warp walks the parts and fills a ring of stages with Y (512 bytes a token)
+// and T and a ring of B tiles (256 rows of B are one contiguous range), and
+// eight consumer warps work on 32 columns each.  Sixteen consecutive tokens
+// are one tensor-map box; others are copied row by row (a copy costs the
+// engine some 35 cycles whatever its size: row copies alone made a prefill
+// chunk 1.6 times slower than plain loads).
+//
+// MMAs have the part's tokens as their 16 rows and 8 columns each; column c of
+// MMA i is column 8 (c / 2) + 2 i + c % 2 of the warp's 32, so a lane's
+// results are eight consecutive columns and 16 bytes of a row of Y and Out.
+// The sums start from Y.  S = 16-rank steps.
 template <int S>
-__global__ void __launch_bounds__(256) lora_expand_kernel(const LoraParams p)
-{
-    __shared__ Groups grp;
-    pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t = lane & 3;
-    const int m0 = blockIdx.z * kBlockTok;
-    // index, B and Y precede the shrink kernel's own wait: readable now
-    const int ngroups = group_tokens(grp, p.index + m0, min(kBlockTok, p.M - m0), p.L);
-    const int n0 = (blockIdx.x * (blockDim.x >> 5) + warp) * 32;
-    const int ncol = n0 + 8 * t;          // first of this lane's eight columns
-    const bool col_in = ncol < p.N;
-    const int quads = p.R / 4;
-    bool waited = false;
+struct Expand {
+    static constexpr int kCols = 256;
+    static constexpr int kConsumers = kCols / 32;
+    static constexpr int kThreads = (kConsumers + 1) * 32;   // + the producer
+    static constexpr int kYRow = kCols * 2;
+    static constexpr int kY = 16 * kYRow, kStage = kY + 16 * 64 * S;   // Y, then T rows of 4 R bytes
+    static constexpr int kStages = S == 1 ? 6 : (S == 2 ? 5 : 4);
+    static constexpr int kBTile = kCols * 32 * S;
+    static constexpr int kBStages = S == 1 ? 4 : (S == 8 ? 2 : 3);
+    static constexpr int kRing = kStages * kStage;
+    static constexpr size_t smem = (size_t)kRing + kBStages * kBTile;
+    // parts that can be filled ahead of T, each with a B of its own
+    static constexpr int kAhead = kStages < kBStages ? kStages : kBStages;
+};
 
-    for (int gi = blockIdx.y; gi < ngroups; gi += gridDim.y) {
-        const int a = grp.g_adapter[gi];
-        const int begin = grp.g_begin[gi], end = grp.g_begin[gi + 1];
-        if (a < 0) {
-            if (p.Out == p.Y)
-                continue;
-            if (!waited)
-                pdl_wait();
-            waited = true;
-            for (int o = begin + g; o < end; o += 8) {
-                const long long m = m0 + grp.list[o];
-                if (col_in)
-                    *reinterpret_cast<uint4 *>(p.Out + m * p.ldo + ncol) =
-                        __ldcg(reinterpret_cast<const uint4 *>(p.Y + m * p.ldy + ncol));
-            }
-            continue;
-        }
-        // B operands: column (row of B) and ranks of this lane.  S = 1: four
-        // consecutive ranks 4 t; else eight, 32 q + 8 t, for two steps
-        uint32_t b[4][S][2];
+// What a part is: its tokens (run: consecutive ones, box: 16 of those),
+// whether its adapter's B is new, whether it has no adapter (Y is copied),
+// whether it is the end of the list.
+struct __align__(16) Part {
+    int rows[16];
+    int ntok, new_b, plain, end;
+    int run, box;
+};
+
+// The parts of one block of tokens.
+struct PartTable {
+    int adapter[kBlockTok];
+    uint8_t ntok[kBlockTok];
+    uint8_t rows[kBlockTok][16];   // offsets in the block, rising
+};
+
+// Fills the table (one warp); returns the number of parts.  Every token finds
+// its place at once, from the masks of its group and a sum over the groups
+// before it: a walk through the groups costs a lone warp a microsecond a part.
+__device__ __forceinline__ int list_parts(const Groups &g, PartTable &tab, bool skip_plain, int lane)
+{
+    const u64 below0 = (1ull << lane) - 1, below1 = (1ull << (lane + 32)) - 1;
+    const int cnt0 = __popcll(g.of0), cnt1 = __popcll(g.of1);
+    const bool lead0 = g.leaders >> lane & 1, lead1 = g.leaders >> (lane + 32) & 1;
+    const int n0 = lead0 && !(skip_plain && g.a0 < 0) ? (cnt0 + 15) / 16 : 0;
+    const int n1 = lead1 && !(skip_plain && g.a1 < 0) ? (cnt1 + 15) / 16 : 0;
+    int s0 = n0, s1 = n1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
-            const uint16_t *row = p.B + ((size_t)a * p.N + n) * p.R;
-            if constexpr (S == 1) {
-                uint2 v = make_uint2(0u, 0u);
-                if (n < p.N && 4 * t < p.R)
-                    v = __ldcg(reinterpret_cast<const uint2 *>(row + 4 * t));
-                b[i][0][0] = v.x;
-                b[i][0][1] = v.y;
-            } else {
-#pragma unroll
-                for (int q = 0; q < S / 2; ++q) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (n < p.N && 32 * q + 8 * t < p.R)
-                        v = ldg128_once(row + 32 * q + 8 * t);
-                    b[i][2 * q][0] = v.x;
-                    b[i][2 * q][1] = v.y;
-                    b[i][2 * q + 1][0] = v.z;
-                    b[i][2 * q + 1][1] = v.w;
-                }
-            }
-        }
-        for (int o = begin; o < end; o += 16) {
-            const bool in0 = o + g < end, in1 = o + g + 8 < end;
-            const long long ma = in0 ? m0 + grp.list[o + g] : 0;
-            const long long mb = in1 ? m0 + grp.list[o + g + 8] : 0;
-            uint4 ya = make_uint4(0u, 0u, 0u, 0u), yb = ya;
-            if (in0 && col_in)
-                ya = __ldcg(reinterpret_cast<const uint4 *>(p.Y + ma * p.ldy + ncol));
-            if (in1 && col_in)
-                yb = __ldcg(reinterpret_cast<const uint4 *>(p.Y + mb * p.ldy + ncol));
-            if (!waited)
-                pdl_wait();   // T is the shrink kernel's
-            waited = true;
-            float acc[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[i][e] = 0.f;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int q = S == 1 ? t : 8 * (s / 2) + 2 * t + (s & 1);   // rank / 4
-                uint4 ta = make_uint4(0u, 0u, 0u, 0u), tb = ta;
-                if (q < quads) {
-                    if (in0)
-                        ta = __ldcg(p.T + ma * quads + q);
-                    if (in1)
-                        tb = __ldcg(p.T + mb * quads + q);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mma_bf16_16816(acc[i], ta.x, tb.x, ta.y, tb.y, b[i][s][0], b[i][s][1]);
-                    mma_bf16_16816(acc[i], ta.z, tb.z, ta.w, tb.w, b[i][s][0], b[i][s][1]);
-                }
-            }
-            const uint32_t y0[4] = {ya.x, ya.y, ya.z, ya.w}, y1[4] = {yb.x, yb.y, yb.z, yb.w};
-            uint32_t w0[4], w1[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w0[i] = f32_to_bf16_bits(__uint_as_float(y0[i] << 16) + acc[i][0]) |
-                        ((uint32_t)f32_to_bf16_bits(__uint_as_float(y0[i] & 0xFFFF0000u) + acc[i][1])
-                         << 16);
-                w1[i] = f32_to_bf16_bits(__uint_as_float(y1[i] << 16) + acc[i][2]) |
-                        ((uint32_t)f32_to_bf16_bits(__uint_as_float(y1[i] & 0xFFFF0000u) + acc[i][3])
-                         << 16);
-            }
-            if (in0 && col_in)
-                *reinterpret_cast<uint4 *>(p.Out + ma * p.ldo + ncol) =
-                    make_uint4(w0[0], w0[1], w0[2], w0[3]);
-            if (in1 && col_in)
-                *reinterpret_cast<uint4 *>(p.Out + mb * p.ldo + ncol) =
-                    make_uint4(w1[0], w1[1], w1[2], w1[3]);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u0 = __shfl_up_sync(0xffffffffu, s0, o), u1 = __shfl_up_sync(0xffffffffu, s1, o);
+        if (lane >= o) {
+            s0 += u0;
+            s1 += u1;
         }
     }
-    // this kernel does not complete before the shrink kernel, even without
-    // any group to work on: what follows on the stream may change the inputs
-    if (!waited)
-        pdl_wait();
+    const int total0 = __shfl_sync(0xffffffffu, s0, 31);
+    const int first0 = s0 - n0, first1 = total0 + s1 - n1;   // of the groups these lanes lead
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const u64 of = h ? g.of1 : g.of0;
+        const int a = h ? g.a1 : g.a0;
+        const int lead = of ? __ffsll(of) - 1 : 0;
+        const int f0 = __shfl_sync(0xffffffffu, first0, lead & 31);
+        const int f1 = __shfl_sync(0xffffffffu, first1, lead & 31);
+        const int first = lead < 32 ? f0 : f1;
+        if (a == -2 || (skip_plain && a < 0))
+            continue;
+        const int rank = __popcll(of & (h ? below1 : below0));
+        tab.rows[first + rank / 16][rank % 16] = (uint8_t)(lane + 32 * h);
+        if (rank % 16 == 0) {
+            tab.adapter[first + rank / 16] = a;
+            tab.ntok[first + rank / 16] = (uint8_t)min(16, __popcll(of) - rank);
+        }
+    }
+    __syncwarp();
+    return total0 + __shfl_sync(0xffffffffu, s1, 31);
+}
+
+template <int S>
+__global__ void __launch_bounds__(Expand<S>::kThreads)
+    lora_expand_kernel(const __grid_constant__ CUtensorMap y_map, const LoraParams p, int blocks,
+                       int subs)
+{
+    using C = Expand<S>;
+    __shared__ Part parts[C::kStages];
+    __shared__ uint64_t full[C::kStages], empty[C::kStages];
+    __shared__ uint64_t b_full[C::kBStages], b_empty[C::kBStages];
+    __shared__ PartTable table;
+    extern __shared__ __align__(128) uint8_t dyn[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n0 = blockIdx.x * C::kCols;
+    const int cols = min(C::kCols, p.N - n0);
+    const int quads = p.R / 4;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], C::kConsumers);
+        }
+        for (int i = 0; i < C::kBStages; ++i) {
+            mbar_init(&b_full[i], 1);
+            mbar_init(&b_empty[i], C::kConsumers);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    // by whole warps; once a wait has run out the role goes to its end
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs));
+        if (!ok && lane == 0)
+            record_error(p.hdr, MXG_ERR_TIMEOUT, where);
+    };
+
+    if (warp == C::kConsumers) {
+        // ------------------------------------------------------- producer
+        int block, block_end, sub = 0;
+        if (subs > 1) {
+            block = blockIdx.y % blocks;
+            block_end = block + 1;
+            sub = blockIdx.y / blocks;
+        } else {
+            block = (int)((long long)blockIdx.y * blocks / gridDim.y);
+            block_end = (int)((long long)(blockIdx.y + 1) * blocks / gridDim.y);
+        }
+        // the index of the next block, ahead of its use
+        int raw0, raw1;
+        auto peek = [&](int b) {
+            const int m = b * kBlockTok + lane;
+            raw0 = b < block_end && m < p.M ? __ldcg(p.index + m) : -1;
+            raw1 = b < block_end && m + 32 < p.M ? __ldcg(p.index + m + 32) : -1;
+        };
+        peek(block);
+        const bool in_place = p.Out == p.Y;
+        const uint64_t pol_once = l2_policy_evict_first(), pol_keep = l2_policy_evict_last();
+        int slot = 0, b_slot = 0;
+        uint32_t phase = 1, b_phase = 1;     // of the empty barriers: the first round is free
+        auto copy_t = [&](int s) {
+            const Part &q = parts[s];
+            const int i = lane - 16;
+            if (q.plain || i < 0 || i >= (q.run ? 1 : q.ntok))
+                return;
+            bulk_g2s(dyn + s * C::kStage + C::kY + i * quads * 16,
+                     p.T + (size_t)q.rows[i] * quads, (q.run ? q.ntok : 1) * quads * 16, &full[s],
+                     pol_keep);
+        };
+        bool waited = false;
+        int before = 0;   // stages filled ahead of the wait: their T comes after it
+        auto wait_shrink = [&]() {
+            // T is the shrink kernel's.  Without any part too: this kernel must
+            // not complete before that one, whose inputs the next on the
+            // stream may change
+            pdl_wait();
+            waited = true;
+            for (int s = 0; s < before; ++s)
+                copy_t(s);
+        };
+        uint32_t filled = 0, b_filled = 0;       // slots with copies issued ...
+        uint32_t parity = 0, b_parity = 0;       // ... and the parity of their last fill
+        int a_last = -1;
+        for (; block < block_end && ok; ++block) {
+            const int m0 = block * kBlockTok;
+            // a whole block of one adapter (a prefill chunk's) needs no list
+            const int a0 = __shfl_sync(0xffffffffu, raw0, 0);
+            const bool one = m0 + kBlockTok <= p.M &&
+                             __all_sync(0xffffffffu, raw0 == a0 && raw1 == a0);
+            int nparts;
+            if (one) {
+                nparts = (a0 < 0 || a0 >= p.L) && in_place ? 0 : kBlockTok / 16;
+            } else {
+                const Groups grp = group_tokens(raw0, raw1, min(kBlockTok, p.M - m0), p.L, lane);
+                __syncwarp();
+                nparts = list_parts(grp, table, in_place, lane);
+            }
+            peek(block + 1);
+            for (int i = sub; i < nparts; i += subs) {
+                if (!waited && before == C::kAhead)
+                    wait_shrink();
+                int a = a0 < p.L ? a0 : -1, n = 16, first = m0 + 16 * i, mine = first + lane;
+                bool run = true;
+                if (!one) {
+                    a = table.adapter[i];
+                    n = table.ntok[i];
+                    first = m0 + table.rows[i][0];
+                    mine = m0 + table.rows[i][lane < n ? lane : 0];
+                    run = m0 + table.rows[i][n - 1] - first == n - 1;
+                }
+                const bool box = run && n == 16;
+                const bool new_b = a >= 0 && a != a_last;
+                wait(&empty[slot], phase, 501);
+                if (!ok)
+                    break;
+                filled |= 1u << slot;
+                parity = (parity & ~(1u << slot)) | ((phase ^ 1u) << slot);
+                Part &q = parts[slot];
+                if (lane < 16)
+                    q.rows[lane] = mine;
+                if (lane == 0) {
+                    *reinterpret_cast<int4 *>(&q.ntok) = make_int4(n, new_b, a < 0, 0);
+                    q.run = run;
+                    q.box = box;
+                }
+                __syncwarp();
+                // a box is written whole: zeros stand for its columns past the end
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[slot], n * ((box ? C::kCols : cols) * 2 +
+                                                            (a < 0 ? 0 : quads * 16)));
+                __syncwarp();
+                // index, B and Y precede the shrink kernel's own wait: they are
+                // read ahead of this kernel's
+                if (box) {
+                    if (lane == 0)
+                        tma_load_2d(dyn + slot * C::kStage, &y_map, n0, first, &full[slot],
+                                    pol_once);
+                } else if (lane < n) {
+                    bulk_g2s(dyn + slot * C::kStage + lane * C::kYRow, p.Y + mine * p.ldy + n0,
+                             cols * 2, &full[slot], pol_once);
+                }
+                if (waited)
+                    copy_t(slot);
+                else
+                    ++before;
+                if (new_b) {
+                    a_last = a;
+                    wait(&b_empty[b_slot], b_phase, 502);
+                    if (!ok)
+                        break;
+                    b_filled |= 1u << b_slot;
+                    b_parity = (b_parity & ~(1u << b_slot)) | ((b_phase ^ 1u) << b_slot);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&b_full[b_slot], cols * p.R * 2);
+                        bulk_g2s(dyn + C::kRing + b_slot * C::kBTile,
+                                 p.B + ((size_t)a * p.N + n0) * p.R, cols * p.R * 2,
+                                 &b_full[b_slot], pol_keep);
+                    }
+                    if (++b_slot == C::kBStages) {
+                        b_slot = 0;
+                        b_phase ^= 1;
+                    }
+                }
+                if (++slot == C::kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!waited)
+            wait_shrink();
+        if (ok)
+            wait(&empty[slot], phase, 503);
+        if (ok) {
+            // the end of the list
+            if (lane == 0) {
+                parts[slot].end = 1;
+                parts[slot].ntok = 0;
+                mbar_arrive(&full[slot]);
+            }
+        } else {
+            // no role works on: every copy issued here has landed before the
+            // CTA exits (otherwise the consumers wait for each of them)
+            for (int s = 0; s < C::kStages; ++s)
+                if (filled >> s & 1)
+                    mbar_wait(&full[s], parity >> s & 1, kWaitLimitNs);
+            for (int s = 0; s < C::kBStages; ++s)
+                if (b_filled >> s & 1)
+                    mbar_wait(&b_full[s], b_parity >> s & 1, kWaitLimitNs);
+        }
+    } else {
+        // ------------------------------------------------------- consumers
+        const int g = lane >> 2, t = lane & 3;
+        uint32_t b[4][S][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                b[i][s][0] = b[i][s][1] = 0;
+        const uint32_t base = smem_u32(dyn);
+        const int ncol = n0 + warp * 32 + 8 * t;
+        const bool col_in = ncol < p.N;
+        const uint32_t yoff = g * C::kYRow + warp * 64 + t * 16, toff = C::kY + g * quads * 16;
+        int slot = 0, b_slot = 0;
+        uint32_t phase = 0, b_phase = 0;
+        while (true) {
+            wait(&full[slot], phase, 521);
+            const int4 q = *reinterpret_cast<const int4 *>(&parts[slot].ntok);
+            if (!ok || q.w)   // end
+                break;
+            const uint32_t st = base + slot * C::kStage;
+            if (q.y) {   // new B
+                wait(&b_full[b_slot], b_phase, 522);
+                if (!ok)
+                    break;
+                // column (row of B) and ranks of this lane.  S = 1: four
+                // consecutive ranks 4 t; else eight, 32 q + 8 t, for two steps
+                const uint32_t tile = base + C::kRing + b_slot * C::kBTile;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t brow =
+                        tile + (warp * 32 + 8 * (g >> 1) + 2 * i + (g & 1)) * p.R * 2;
+                    if constexpr (S == 1) {
+                        const uint2 v = 4 * t < p.R ? lds64a(brow + 8 * t) : make_uint2(0u, 0u);
+                        b[i][0][0] = v.x;
+                        b[i][0][1] = v.y;
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < S / 2; ++h) {
+                            const uint4 v = 32 * h + 8 * t < p.R ? lds128a(brow + 64 * h + 16 * t)
+                                                                 : make_uint4(0u, 0u, 0u, 0u);
+                            b[i][2 * h][0] = v.x;
+                            b[i][2 * h][1] = v.y;
+                            b[i][2 * h + 1][0] = v.z;
+                            b[i][2 * h + 1][1] = v.w;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&b_empty[b_slot]);
+                if (++b_slot == C::kBStages) {
+                    b_slot = 0;
+                    b_phase ^= 1;
+                }
+            }
+            const int2 row =
+                make_int2(g < q.x ? parts[slot].rows[g] : -1, g + 8 < q.x ? parts[slot].rows[g + 8] : -1);
+            const uint4 y[2] = {lds128a(st + yoff), lds128a(st + yoff + 8 * C::kYRow)};
+            uint32_t w[2][4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                w[r][0] = y[r].x;
+                w[r][1] = y[r].y;
+                w[r][2] = y[r].z;
+                w[r][3] = y[r].w;
+            }
+            if (!q.z) {   // with an adapter
+                float acc[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][e] = __uint_as_float(e & 1 ? w[e >> 1][i] & 0xFFFF0000u
+                                                          : w[e >> 1][i] << 16);
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const int r4 = S == 1 ? t : 8 * (s / 2) + 2 * t + (s & 1);   // rank / 4
+                    uint4 ta = make_uint4(0u, 0u, 0u, 0u), tb = ta;
+                    if (r4 < quads) {
+                        ta = lds128a(st + toff + 16 * r4);
+                        tb = lds128a(st + toff + (8 * quads + r4) * 16);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mma_bf16_16816(acc[i], ta.x, tb.x, ta.y, tb.y, b[i][s][0], b[i][s][1]);
+                        mma_bf16_16816(acc[i], ta.z, tb.z, ta.w, tb.w, b[i][s][0], b[i][s][1]);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[r][i] = pack_bf16(acc[i][2 * r], acc[i][2 * r + 1]);
+            }
+            // every lane's reads of the stage have returned: it is free
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&empty[slot]);
+            if (col_in && row.x >= 0)
+                *reinterpret_cast<uint4 *>(p.Out + row.x * p.ldo + ncol) =
+                    make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+            if (col_in && row.y >= 0)
+                *reinterpret_cast<uint4 *>(p.Out + row.y * p.ldo + ncol) =
+                    make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+            if (++slot == C::kStages) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+    }
 }
 
 // Attributes a kernel launch needs, set once per device.
@@ -430,12 +777,11 @@ cudaError_t allow_smem(const void *fn, std::atomic<bool> (&done)[kMaxDeviceCache
     return cudaSuccess;
 }
 
-template <int RT, int NT>
+template <int RT>
 cudaError_t launch_shrink(const LoraPlan &pl, const LoraParams &p, cudaStream_t stream)
 {
-    const void *fn = reinterpret_cast<const void *>(&lora_shrink_kernel<RT, NT>);
-    constexpr size_t smem =
-        (size_t)kShrinkWarps * RT * NT * 512 + (size_t)8 * NT * (16 * RT + 4) * sizeof(float);
+    const void *fn = reinterpret_cast<const void *>(&lora_shrink_kernel<RT>);
+    constexpr size_t smem = Shrink<RT>::smem;
     static std::atomic<bool> done[kMaxDeviceCache];
     const cudaError_t e = allow_smem(fn, done, smem);
     if (e != cudaSuccess)
@@ -444,6 +790,28 @@ cudaError_t launch_shrink(const LoraPlan &pl, const LoraParams &p, cudaStream_t 
     void *args[] = {&q};
     return launch_pdl_cluster(fn, dim3(pl.cluster, pl.shrink_subs, pl.blocks * pl.slices),
                               dim3(kShrinkWarps * 32), pl.cluster, smem, stream, args);
+}
+
+template <int S>
+cudaError_t launch_expand(const LoraPlan &pl, const LoraParams &p, cudaStream_t stream)
+{
+    const void *fn = reinterpret_cast<const void *>(&lora_expand_kernel<S>);
+    static std::atomic<bool> done[kMaxDeviceCache];
+    const cudaError_t e = allow_smem(fn, done, Expand<S>::smem);
+    if (e != cudaSuccess)
+        return e;
+    // boxes of 16 tokens x 256 columns (a batch of fewer tokens has none)
+    alignas(64) CUtensorMap ym{};
+    if (p.M >= 16 &&
+        !encode_tensor_map_2d(&ym, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y, (uint64_t)p.N,
+                              (uint64_t)p.M, (uint64_t)p.ldy * 2, Expand<S>::kCols, 16,
+                              CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    LoraParams q = p;
+    int blocks = pl.blocks, subs = pl.expand_subs;
+    void *args[] = {&ym, &q, &blocks, &subs};
+    return launch_pdl(fn, dim3(pl.ntiles, pl.expand_shares), dim3(Expand<S>::kThreads),
+                      Expand<S>::smem, stream, args);
 }
 
 }  // namespace
@@ -457,7 +825,7 @@ bool lora_shape_ok(int M, int N, int K, int R)
 
 size_t lora_scratch_bytes(int M, int R)
 {
-    return (size_t)M * R * 4;
+    return sizeof(WsHeader) + (size_t)M * R * 4;
 }
 
 LoraPlan plan_lora(int device, int M, int N, int K, int R)
@@ -469,23 +837,30 @@ LoraPlan plan_lora(int device, int M, int N, int K, int R)
     pl.slices = (R + 16 * pl.rank_tiles - 1) / (16 * pl.rank_tiles);
     pl.blocks = (int)blocks;
     const int tok = std::min(M, kBlockTok);
-    // shrink: K is split over a cluster while the blocks alone leave SMs idle
-    // (two CTAs fit on one), with at least a unit of 32 k per warp
-    const int units = (K + 31) / 32;
+    // shrink: K is split over a cluster while the blocks alone leave room (two
+    // CTAs fit on an SM), with at least 32 k a warp
     pl.cluster = 1;
     while (pl.cluster < 8 && 2 * pl.cluster * blocks * pl.slices <= 2 * sms &&
-           2 * pl.cluster * kShrinkWarps <= units)
+           2 * pl.cluster * kShrinkWarps * 32 <= K)
         pl.cluster *= 2;
-    // groups of a block run side by side while there is room for them: the
-    // host does not know how many there are, and a share without any ends at
-    // once
+    // groups of a block run side by side in what room is left: the host does
+    // not know how many there are, and a share without any ends at once
     const long long shrink_ctas = blocks * pl.slices * pl.cluster;
-    pl.shrink_subs = (int)std::max<long long>(1, std::min<long long>(tok, 4 * sms / shrink_ctas));
-    // expand: 128 columns a CTA while that leaves SMs idle, else 256
-    pl.expand_warps = ((N + 255) / 256) * blocks < sms ? 4 : 8;
-    pl.ntiles = (N + 32 * pl.expand_warps - 1) / (32 * pl.expand_warps);
-    const long long expand_ctas = blocks * pl.ntiles;
-    pl.expand_subs = (int)std::max<long long>(1, std::min<long long>(tok, 8 * sms / expand_ctas));
+    pl.shrink_subs = (int)std::max<long long>(1, std::min<long long>(tok, 2 * sms / shrink_ctas));
+    // expand: one wave of CTAs; they share the blocks out, or, with fewer
+    // blocks than that, each block's groups
+    const int steps = (R + 15) / 16;
+    pl.expand_steps = steps <= 2 ? steps : (steps <= 4 ? 4 : 8);
+    pl.ntiles = (N + 255) / 256;
+    const int fit = pl.expand_steps <= 2 ? 2 : 1;   // CTAs an SM
+    const int shares = std::max(1, fit * sms / pl.ntiles);
+    if (shares <= blocks) {
+        pl.expand_subs = 1;
+        pl.expand_shares = shares;
+    } else {
+        pl.expand_subs = std::min(tok, (int)(shares / blocks));
+        pl.expand_shares = (int)(pl.expand_subs * blocks);
+    }
     return pl;
 }
 
@@ -499,7 +874,8 @@ cudaError_t launch_lora(const LoraPlan &pl, const LoraArgs &a, cudaStream_t stre
     p.Out = static_cast<uint16_t *>(a.Out);
     p.scales = a.scales;
     p.index = a.index;
-    p.T = static_cast<uint4 *>(a.workspace);
+    p.hdr = static_cast<WsHeader *>(a.workspace);
+    p.T = reinterpret_cast<uint4 *>(p.hdr + 1);
     p.ldx = a.ldx;
     p.ldy = a.ldy;
     p.ldo = a.ldo;
@@ -510,21 +886,19 @@ cudaError_t launch_lora(const LoraPlan &pl, const LoraArgs &a, cudaStream_t stre
     p.L = a.L;
     cudaError_t e;
     if (pl.rank_tiles == 1)
-        e = launch_shrink<1, 8>(pl, p, stream);
+        e = launch_shrink<1>(pl, p, stream);
     else if (pl.rank_tiles == 2)
-        e = launch_shrink<2, 8>(pl, p, stream);
+        e = launch_shrink<2>(pl, p, stream);
     else
-        e = launch_shrink<4, 4>(pl, p, stream);
+        e = launch_shrink<4>(pl, p, stream);
     if (e != cudaSuccess)
         return e;
-    const int steps = (a.R + 15) / 16;
-    const void *fn = steps == 1   ? reinterpret_cast<const void *>(&lora_expand_kernel<1>)
-                     : steps == 2 ? reinterpret_cast<const void *>(&lora_expand_kernel<2>)
-                     : steps <= 4 ? reinterpret_cast<const void *>(&lora_expand_kernel<4>)
-                                  : reinterpret_cast<const void *>(&lora_expand_kernel<8>);
-    void *args[] = {&p};
-    return launch_pdl(fn, dim3(pl.ntiles, pl.expand_subs, pl.blocks), dim3(32 * pl.expand_warps), 0,
-                      stream, args);
+    switch (pl.expand_steps) {
+    case 1: return launch_expand<1>(pl, p, stream);
+    case 2: return launch_expand<2>(pl, p, stream);
+    case 4: return launch_expand<4>(pl, p, stream);
+    default: return launch_expand<8>(pl, p, stream);
+    }
 }
 
 }  // namespace mxg

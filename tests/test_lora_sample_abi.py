@@ -6,7 +6,16 @@ import ctypes
 import pytest
 import torch
 
-from test_binding_marshal import _val, bf16, fake  # noqa: F401  (fixture)
+from test_binding_marshal import _val, bf16, fake as fake_lib  # noqa: F401  (fixture)
+
+
+
+@pytest.fixture()
+def fake(fake_lib, monkeypatch):  # noqa: F811
+    """The recording library, with CPU tensors let through."""
+    monkeypatch.setattr(fake_lib[0], "_need_cuda", lambda t, name: None)
+    return fake_lib
+
 
 P = ctypes.c_void_p
 OK, INVALID, SHAPE, WORKSPACE = 0, -1, -2, -3
@@ -46,9 +55,9 @@ def test_lora_refusals(lib):
     for bad in (dict(R=0), dict(R=4), dict(R=12), dict(R=136), dict(N=0, ldy=256), dict(N=252),
                 dict(K=508), dict(K=0), dict(M=2097089), dict(K=-8), dict(N=-8)):
         assert lora(lib, **bad) == SHAPE, bad
-    assert lora(lib, bytes=4 * 16 * 4 - 1) == WORKSPACE
-    assert lib.lora_workspace_bytes(4, 256, 512, 16) == 4 * 16 * 4
-    assert lib.lora_workspace_bytes(2097088, 8, 8, 128) == 2097088 * 512
+    assert lora(lib, bytes=256 + 4 * 16 * 4 - 1) == WORKSPACE
+    assert lib.lora_workspace_bytes(4, 256, 512, 16) == 256 + 4 * 16 * 4
+    assert lib.lora_workspace_bytes(2097088, 8, 8, 128) == 256 + 2097088 * 512
     for bad in ((0, 256, 512, 16), (4, 250, 512, 16), (4, 256, 511, 16), (4, 256, 512, 15),
                 (4, 256, 512, 256)):
         assert lib.lora_workspace_bytes(*bad) == 0
@@ -73,7 +82,7 @@ def test_sample_refusals(lib):
         assert sample(lib, **bad) == SHAPE, bad
 
 
-def test_lora_binding(fake):  # noqa: F811
+def test_lora_binding(fake):
     m, lib = fake
     x, a, b, y = bf16(3, 64), bf16(2, 16, 64), bf16(2, 40, 16), bf16(3, 40)
     index, s = torch.zeros(3, dtype=torch.int32), torch.ones(2)
@@ -83,7 +92,7 @@ def test_lora_binding(fake):  # noqa: F811
     got = [_val(v) for v in args[:-1]]
     assert got[:15] == [x.data_ptr(), 64, a.data_ptr(), b.data_ptr(), s.data_ptr(),
                         index.data_ptr(), y.data_ptr(), 40, out.data_ptr(), 40, 3, 40, 64, 16, 2]
-    assert got[16] == 3 * 16 * 4 and args[-1] == ("stream", None, x.device)
+    assert got[16] == 256 + 3 * 16 * 4 and args[-1] == ("stream", None, x.device)
     # in place, on a column range
     wide = bf16(3, 128)
     part = wide[:, 40:80]
@@ -114,7 +123,7 @@ def test_lora_binding(fake):  # noqa: F811
             m.lora_add(bf16(3, K), bf16(2, R, K), bf16(2, N, R), index, bf16(3, N))
 
 
-def test_sample_binding(fake):  # noqa: F811
+def test_sample_binding(fake):
     m, lib = fake
     logits, u = bf16(3, 50), torch.zeros(3)
     k, p = torch.zeros(3, dtype=torch.int32), torch.ones(3)
@@ -142,7 +151,7 @@ def test_sample_binding(fake):  # noqa: F811
             m.sample_logits(**{**good, **bad})
 
 
-def test_head_and_sampler_binding(fake):  # noqa: F811
+def test_head_and_sampler_binding(fake):
     m, lib = fake
     packed = torch.zeros(int(m._lib._real.w8a16_packed_bytes(128, 192, 128)), dtype=torch.uint8)
     u = torch.zeros(2)
