@@ -382,7 +382,7 @@ MXG_API int bf16_gemm_small_ex(const void *X, const void *W, int M, int N, int K
  * GEMMs, nothing is read before the previous kernel on `stream` has
  * completed: A, B and index may be what it writes.
  * 1 <= M <= 2097088; K, N, R >= 8 and multiples of 8; R <= 128;
- * strides multiples of 8.  Other sizes: MXG_ERR_UNSUPPORTED_SHAPE; a stride
+ * L * R < 2^31; strides multiples of 8.  Other sizes: MXG_ERR_UNSUPPORTED_SHAPE; a stride
  * below its row or not a multiple of 8, L < 1: MXG_ERR_INVALID_ARG. */
 MXG_API size_t lora_workspace_bytes(int M, int N, int K, int R);
 MXG_API int lora_add(const void *X, long long ldx, const void *A, const void *B,

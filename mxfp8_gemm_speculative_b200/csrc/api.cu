@@ -561,7 +561,7 @@ int lora_add(const void *X, long long ldx, const void *A, const void *B, const f
         return MXG_ERR_INVALID_ARG;
     if (ldx < K || ldy < N || ldo < N || ldx % 8 || ldy % 8 || ldo % 8 || (Out == Y && ldo != ldy))
         return MXG_ERR_INVALID_ARG;
-    if (!lora_shape_ok(M, N, K, R))
+    if (!lora_shape_ok(M, N, K, R) || (long long)L * R > 0x7fffffffLL)
         return MXG_ERR_UNSUPPORTED_SHAPE;
     if (workspace_bytes < lora_scratch_bytes(M, R))
         return MXG_ERR_WORKSPACE;

@@ -109,8 +109,9 @@ cudaError_t launch_bf16_small(const SmallPlan &plan, const void *X, const void *
 // ------------------------------------------------------ low-rank adapters
 struct LoraPlan {
     int blocks;           // blocks of 64 tokens
-    int rank_tiles;       // 16-rank tiles a shrink CTA holds (1, 2, 4)
-    int slices;           // rank slices of that many tiles
+    int slices;           // rank slices (shrink)
+    int slice_ranks;      // ranks of a slice (the last may have fewer)
+    int rank_tiles;       // 16-rank tiles of the shrink variant (1, 2, 4)
     int cluster;          // CTAs that split K (shrink)
     int shrink_subs, expand_subs;   // CTAs that share a block's groups
     int expand_steps;     // 16-rank steps of the expand variant (1, 2, 4, 8)

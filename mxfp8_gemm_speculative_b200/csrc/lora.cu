@@ -25,6 +25,7 @@
 // once in all for a decode batch.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -56,14 +57,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool i
                  "r"(in ? 16 : 0)
                  : "memory");
 }
-__device__ __forceinline__ void cp_async_commit()
+// Arrives on a barrier once the thread's asynchronous copies so far have landed
+// (one of the barrier's expected arrivals).
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
 {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 
 // -------------------------------------------------------- tokens by adapter
@@ -154,68 +153,46 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 }
 
 // ------------------------------------------------------------------- shrink
-// One cluster per (block of tokens, share of its groups, slice of 16 RT
-// ranks); its CTAs split K and are added through distributed shared memory in
-// rank order (bitwise reproducible; no atomics, no partial sums in memory).
-// A CTA streams its K range of a group's rows of X (gathered by token) and of
-// the adapter's rows of A through a ring of 64-k stages in shared memory,
-// filled by asynchronous copies.  MMAs have the ranks as their 16 rows and 8
-// tokens as their columns; a warp takes one 32-k half of every stage, and the
-// halves are added at the end.  A group of up to 16 tokens (decode and verify
-// chunks, where the bytes of A are what counts) takes smaller stages and more
-// of them: in flight is what covers the latency.  Neither that choice nor a
-// token's place in the batch changes the order of its sums.
+// One cluster per (block of tokens, share of its groups, slice of ranks); its
+// CTAs split K and are added through distributed shared memory in rank order
+// (bitwise reproducible; no atomics, no partial sums in memory).  A producer
+// warp streams a CTA's K range of a group's rows of X and of the adapter's
+// rows of A through a ring in shared memory: A (and X, for a run of more than
+// 16 tokens) as tensor-map boxes of 64 k, other rows of X by asynchronous
+// copies of 16 bytes.  Eight consumer warps run MMAs with the ranks as their
+// 16 rows and 8 tokens as their columns; a warp takes every other 16 bytes of
+// a row, and the two halves are added at the end.
+//
+// Up to 16 tokens (decode and verify chunks) the bytes of A are what counts,
+// and a stage holds more k of fewer rows.  Neither that nor a token's place
+// in the batch changes the order of its sums.
 template <int RT>
 struct Shrink {
-    // stages of `rows` tokens: 64 k of each and of the ranks
-    static constexpr int stage(int rows) { return (rows + 16 * RT) * 128; }
-    static constexpr int kManyStages = 5, kFewStages = RT == 1 ? 12 : 8;
-    static constexpr int kMany = kManyStages * stage(kBlockTok), kFewRing = kFewStages * stage(kFew);
-    static constexpr int kRing = kMany > kFewRing ? kMany : kFewRing;
-    static constexpr int ST = 16 * RT + 4;                 // row stride of the reduced tile
-    static constexpr int kTile = kBlockTok * ST * (int)sizeof(float);
-    static_assert(kTile <= kRing, "the second halves go into the ring");
-    static constexpr size_t smem = (size_t)kRing + kTile;
+    static constexpr int kTok = RT == 4 ? 32 : 64;          // tokens of a group at a time
+    static constexpr int sub(int rows) { return (rows + 16 * RT) * 128; }   // 64 k of tokens, ranks
+    static constexpr int kSubMany = RT == 1 ? 2 : 1, kSubFew = RT == 1 ? 4 : (RT == 2 ? 2 : 1);   // per stage
+    static constexpr int kMany = kSubMany * sub(kTok), kFewStage = kSubFew * sub(kFew);
+    static constexpr int kSlot = kMany > kFewStage ? kMany : kFewStage;
+    static constexpr int kSlots = RT == 1 ? 4 : 7;
+    static constexpr int ST = 16 * RT + 4;                  // row stride of a reduced tile
+    static constexpr int kTile = kTok * ST * (int)sizeof(float);
+    // ring (aligned to 1024 bytes), tiles of the two halves
+    static constexpr size_t smem = (size_t)kSlots * kSlot + 2 * kTile + 1024;
+    static constexpr int kThreads = (kShrinkWarps + 1) * 32;
 };
 
-// The inner products of `ntok` <= ROWS tokens (offsets from x in `list`) with
-// the ranks of a slice (`ranks` rows of `arow`) over k0 .. k1, into
-// tile[token][rank].
-template <int RT, int ROWS, int STAGES>
-__device__ __forceinline__ void shrink_group(const LoraParams &p, const uint16_t *x,
-                                             const uint8_t *list, int ntok, const uint16_t *arow,
-                                             int ranks, int k0, int k1, uint8_t *ring, float *tile)
+// The consumers' part of one item: MMAs over the stages of up to ROWS tokens.
+template <int RT, int ROWS, int SUB, typename W>
+__device__ __forceinline__ void shrink_item(int ntok, int k0, int k1, uint32_t ring, float *tile,
+                                            uint64_t *empty, int &slot, uint32_t &phase, W &&wait,
+                                            const bool &ok)
 {
     using C = Shrink<RT>;
-    constexpr int kStage = C::stage(ROWS), kXStage = ROWS * 128;
-    constexpr int kTiles = ROWS / 8;                              // of 8 tokens
-    constexpr int kPer = (kTiles + kShrinkWarps / 2 - 1) / (kShrinkWarps / 2);   // per warp
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kHalf = kShrinkWarps / 2;
+    constexpr int kPer = (ROWS / 8 + kHalf - 1) / kHalf;   // token tiles per warp
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int q = warp / (kShrinkWarps / 2), first = warp % (kShrinkWarps / 2);
-    // Stage rows of 128 bytes are eight chunks of 16; chunk c of row r lies at
-    // c ^ 4 (r & 1), so the two rows that eight lanes load together use all
-    // banks.  Rows of absent tokens and ranks are not filled: they only reach
-    // results that nobody reads.
-    const int chunk = tid & 7;
-    auto fill = [&](int k, int slot) {
-        const uint32_t st = smem_u32(ring) + slot * kStage;
-        const int kc = k + 8 * chunk;
-        const bool in = kc < k1;
-        for (int r = tid >> 3; r < ROWS + 16 * RT; r += kShrinkWarps * 4) {
-            const uint16_t *src;
-            if (r < ROWS) {
-                if (r >= ntok)
-                    continue;
-                src = x + list[r] * p.ldx;
-            } else {
-                if (r - ROWS >= ranks)
-                    continue;
-                src = arow + (size_t)(r - ROWS) * p.K;
-            }
-            cp_async16(st + r * 128 + ((chunk ^ (r & 1) << 2) << 4), src + (in ? kc : 0), in);
-        }
-    };
+    const int q = warp / kHalf, first = warp % kHalf;
     float acc[kPer][RT][4];
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
@@ -224,90 +201,91 @@ __device__ __forceinline__ void shrink_group(const LoraParams &p, const uint16_t
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 acc[j][i][e] = 0.f;
-    const int steps = (k1 - k0 + 63) / 64;
+    // Rows of 128 bytes with the 128-byte swizzle: 16-byte chunk c of row r
+    // lies at c ^ (r % 8).  With the chunks 2 t + q, the two rows that eight
+    // lanes load together use all banks.
+    const uint32_t at = g * 128 + (((2 * t + q) ^ g) << 4);
+    for (int k = k0; k < k1; k += 64 * SUB) {
+        wait(slot, phase);
+        if (ok && 8 * first < ntok) {
+            const uint32_t st = ring + slot * C::kSlot + at;
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-        if (s < steps)
-            fill(k0 + 64 * s, s);
-        cp_async_commit();
-    }
-    int slot = 0, next = STAGES - 1;
-    for (int s = 0; s < steps; ++s) {
-        cp_async_wait<STAGES - 2>();
-        __syncthreads();   // stage s is complete, stage s - 1 has been read
-        if (s + STAGES - 1 < steps)
-            fill(k0 + 64 * (s + STAGES - 1), next);
-        cp_async_commit();
-        if (8 * first < ntok) {
-            const uint32_t c = ((4 * q + t) ^ (g & 1) << 2) << 4;
-            const uint32_t st = smem_u32(ring) + slot * kStage + g * 128 + c;
-            uint4 xv[kPer];
+            for (int u = 0; u < SUB; ++u) {
+                if (u > 0 && k + 64 * u >= k1)
+                    break;
+                const uint32_t x = st + u * C::sub(ROWS), a = x + ROWS * 128;
+                uint4 xv[kPer];
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                xv[j] = lds128a(st + 8 * (first + j * (kShrinkWarps / 2)) * 128);
+                for (int j = 0; j < kPer; ++j)
+                    xv[j] = lds128a(x + (first + j * kHalf) * 1024);
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const uint4 a0 = lds128a(st + kXStage + 16 * i * 128);
-                const uint4 a1 = lds128a(st + kXStage + (16 * i + 8) * 128);
+                for (int i = 0; i < RT; ++i) {
+                    const uint4 a0 = lds128a(a + 2 * i * 1024), a1 = lds128a(a + (2 * i + 1) * 1024);
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    mma_bf16_16816(acc[j][i], a0.x, a1.x, a0.y, a1.y, xv[j].x, xv[j].y);
-                    mma_bf16_16816(acc[j][i], a0.z, a1.z, a0.w, a1.w, xv[j].z, xv[j].w);
+                    for (int j = 0; j < kPer; ++j) {
+                        mma_bf16_16816(acc[j][i], a0.x, a1.x, a0.y, a1.y, xv[j].x, xv[j].y);
+                        mma_bf16_16816(acc[j][i], a0.z, a1.z, a0.w, a1.w, xv[j].z, xv[j].w);
+                    }
                 }
             }
         }
-        slot = slot + 1 == STAGES ? 0 : slot + 1;
-        next = next + 1 == STAGES ? 0 : next + 1;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&empty[slot]);
+        if (++slot == C::kSlots) {
+            slot = 0;
+            phase ^= 1;
+        }
     }
-    // the second halves go through the ring, once it has been read, to the first
-    cp_async_wait<0>();
-    __syncthreads();
-    constexpr int ST = C::ST;
-    float *other = reinterpret_cast<float *>(ring);
+    // this warp's half: tile[half][token][rank]
+    float *mine = tile + q * (C::kTile / (int)sizeof(float));
 #pragma unroll
-    for (int pass = 1; pass >= 0; --pass) {
-        if (q == pass)
+    for (int j = 0; j < kPer; ++j) {
+        const int c = 8 * (first + j * kHalf) + 2 * t;
+        if (c - 2 * t < ntok)
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int c = 8 * (first + j * (kShrinkWarps / 2)) + 2 * t;
-                if (c - 2 * t < min(ntok, ROWS))
+            for (int i = 0; i < RT; ++i)
 #pragma unroll
-                    for (int i = 0; i < RT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int at = (c + (e & 1)) * ST + 16 * i + g + 8 * (e >> 1);
-                            if (pass)
-                                other[at] = acc[j][i][e];
-                            else
-                                tile[at] = acc[j][i][e] + other[at];
-                        }
-            }
-        if (pass)
-            __syncthreads();
+                for (int e = 0; e < 4; ++e)
+                    mine[(c + (e & 1)) * C::ST + 16 * i + g + 8 * (e >> 1)] = acc[j][i][e];
     }
 }
 
 template <int RT>
-__global__ void __launch_bounds__(kShrinkWarps * 32, 2) lora_shrink_kernel(const LoraParams p)
+__global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
+    lora_shrink_kernel(const __grid_constant__ CUtensorMap x_map,
+                       const __grid_constant__ CUtensorMap a_map, const LoraParams p, int slices,
+                       int slice_ranks)
 {
     using C = Shrink<RT>;
     constexpr int ST = C::ST;
-    __shared__ uint8_t lists[kShrinkWarps][kBlockTok];
-    extern __shared__ __align__(128) uint8_t dyn[];
-    float *tile = reinterpret_cast<float *>(dyn + C::kRing);   // [tokens][ST]
+    __shared__ uint8_t lists[kShrinkWarps + 1][kBlockTok];
+    __shared__ uint64_t full[C::kSlots], empty[C::kSlots];
+    extern __shared__ uint8_t dyn_raw[];
+    // 1024-byte alignment for the swizzled boxes
+    uint8_t *dyn = dyn_raw + ((1024 - (smem_u32(dyn_raw) & 1023)) & 1023);
+    float *tile = reinterpret_cast<float *>(dyn + C::kSlots * C::kSlot);   // [halves][tokens][ST]
 
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&full[i], 1 + 32);   // the boxes' bytes, and every lane's own copies
+            mbar_init(&empty[i], kShrinkWarps);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
     // The dependent launch is allowed only after this wait: the expand kernel
     // may then read the index, B and Y before its own wait, since everything
     // queued before this kernel has completed.
     pdl_wait();
     pdl_launch_dependents();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0)
         p.hdr->status = p.hdr->where = 0;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nslices = (p.R + 16 * RT - 1) / (16 * RT);
-    const int block = blockIdx.z / nslices, slice = blockIdx.z % nslices;
-    const int m0 = block * kBlockTok, r0 = slice * 16 * RT;
+    const int block = blockIdx.z / slices, slice = blockIdx.z % slices;
+    const int m0 = block * kBlockTok, r0 = slice * slice_ranks;
+    const int ranks = min(slice_ranks, p.R - r0);
     const Groups grp = group_tokens(m0 + lane < p.M ? __ldcg(p.index + m0 + lane) : -1,
                                     m0 + lane + 32 < p.M ? __ldcg(p.index + m0 + lane + 32) : -1,
                                     min(kBlockTok, p.M - m0), p.L, lane);
@@ -317,53 +295,180 @@ __global__ void __launch_bounds__(kShrinkWarps * 32, 2) lora_shrink_kernel(const
     const int k0 = (int)((long long)crank * units / csize) * 64;
     const int k1 = min(p.K, (int)((long long)(crank + 1) * units / csize) * 64);
 
-    int n = 0;   // groups seen so far: this cluster takes every gridDim.y-th
-    for (u64 rest = grp.leaders; rest; rest &= rest - 1) {
-        int a;
-        if (n % (int)gridDim.y != (int)blockIdx.y) {
+    // Every warp walks the items of this cluster, in the same order: every
+    // gridDim.y-th group of the block, kTok tokens at a time.  Each ends with
+    // two cluster barriers that all threads take part in.
+    u64 rest = grp.leaders;
+    int seen = 0, a = -1, ntok = 0, begin = 0;
+    auto next_item = [&]() {
+        begin += C::kTok;
+        if (begin < ntok)
+            return true;
+        while (rest) {
             const int first = __ffsll(rest) - 1;
+            rest &= rest - 1;
             a = __shfl_sync(0xffffffffu, first >= 32 ? grp.a1 : grp.a0, first & 31);
-            n += a >= 0;
-            continue;
+            if (a < 0 || seen++ % (int)gridDim.y != (int)blockIdx.y)
+                continue;
+            ntok = take_group(grp, first, list, lane, a);
+            begin = 0;
+            return true;
         }
-        const int ntok = take_group(grp, __ffsll(rest) - 1, list, lane, a);
-        if (a < 0)
-            continue;
-        ++n;
-        const uint16_t *x = p.X + m0 * p.ldx;
-        const uint16_t *arow = p.A + ((size_t)a * p.R + r0) * p.K;
-        const int ranks = min(16 * RT, p.R - r0);
-        if (ntok <= kFew)
-            shrink_group<RT, kFew, C::kFewStages>(p, x, list, ntok, arow, ranks, k0, k1, dyn, tile);
+        return false;
+    };
+    // waits by whole warps; after one that ran out the role only goes through
+    // the barriers
+    bool ok = true;
+    auto wait_on = [&](uint64_t *bar, uint32_t parity, int where) {
+        if (!ok)
+            return;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs));
+        if (!ok && lane == 0)
+            record_error(p.hdr, MXG_ERR_TIMEOUT, where);
+    };
+
+    if (warp == kShrinkWarps) {
+        // ------------------------------------------------------- producer
+        const uint64_t pol_a = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
+        int slot = 0;
+        uint32_t phase = 1;         // of the empty barriers: the first round is free
+        bool wrapped = false;
+        bool owed = false;          // the last item's barriers
+        auto barriers = [&]() {
+            cluster_barrier();
+            cluster_barrier();
+            owed = false;
+        };
+        // One stage after another, by one warp: everything that does not
+        // change within an item is worked out before its stages.
+        auto stages = [&](auto few_) {
+            constexpr bool kIsFew = decltype(few_)::value;
+            constexpr int kRows = kIsFew ? kFew : C::kTok;
+            constexpr int kSub = kIsFew ? C::kSubFew : C::kSubMany;
+            constexpr int kCopies = kRows / 4;   // rows lane / 8 + 4 i, 16 bytes lane % 8
+            const int n = min(C::kTok, ntok - begin);
+            const int m = m0 + list[begin];
+            // boxes of 16 tokens, for a run (a few rows are as well copied one by one)
+            const bool run = !kIsFew && m0 + list[begin + n - 1] - m == n - 1;
+            const int xb = run ? (n + 15) / 16 : 0;
+            const int copies = run ? 0 : (n + 3) / 4;
+            const int c = lane & 7;
+            const uint16_t *src[kCopies];
+            uint32_t dst[kCopies];
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int r = (lane >> 3) + 4 * i;
+                src[i] = p.X + (m0 + list[begin + (r < n ? r : 0)]) * p.ldx + 8 * c;
+                dst[i] = r * 128 + ((c ^ (r & 7)) << 4);
+            }
+            const int arow = a * p.R + r0;
+            // boxes of this item may land where copies of rows did
+            fence_proxy_async_smem();
+            int s = 0;
+            for (int k = k0; k < k1; k += 64 * kSub, ++s) {
+                // the ring may run ahead of the last item's end by its own size
+                if (owed && s == C::kSlots)
+                    barriers();
+                wait_on(&empty[slot], phase, 531);
+                if (!ok)
+                    break;
+                const int nsub = kSub == 1 ? 1 : min(kSub, (k1 - k + 63) / 64);
+                uint8_t *st = dyn + slot * C::kSlot;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[slot], nsub * (slice_ranks + 16 * xb) * 128);
+                __syncwarp();
+                if (lane < nsub)
+                    tma_load_2d(st + lane * C::sub(kRows) + kRows * 128, &a_map, k + 64 * lane, arow,
+                                &full[slot], pol_a);
+                if (!kIsFew && lane < kSub * (kRows / 16)) {
+                    const int u = lane / (kRows / 16), j = lane % (kRows / 16);
+                    if (u < nsub && j < xb)
+                        tma_load_2d(st + u * C::sub(kRows) + j * 2048, &x_map, k + 64 * u,
+                                    m + 16 * j, &full[slot], pol_x);
+                }
+                if (copies > 0) {
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u) {
+                        if (u >= nsub)
+                            break;
+                        const int kc = k + 64 * u;
+                        const bool in = kc + 8 * c < p.K;
+#pragma unroll
+                        for (int i = 0; i < kCopies; ++i) {
+                            if (i >= copies)
+                                break;
+                            if ((lane >> 3) + 4 * i < n)
+                                cp_async16(smem_u32(st) + u * C::sub(kRows) + dst[i],
+                                           in ? src[i] + kc : src[i] - 8 * c, in);
+                        }
+                    }
+                }
+                cp_async_arrive(&full[slot]);
+                if (++slot == C::kSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                    wrapped = true;
+                }
+            }
+        };
+        while (next_item()) {
+            if (min(C::kTok, ntok - begin) <= kFew)
+                stages(std::true_type());
+            else
+                stages(std::false_type());
+            if (owed)
+                barriers();
+            owed = true;
+        }
+        if (owed)
+            barriers();
+        // (otherwise the consumers wait for every copy issued here)
+        if (!ok)
+            for (int s = 0; s < C::kSlots; ++s)
+                if (s < slot || wrapped)
+                    mbar_wait(&full[s], s < slot ? phase ^ 1 : phase, kWaitLimitNs);
+        return;
+    }
+
+    int slot = 0;
+    uint32_t phase = 0;
+    auto wait_full = [&](int s, uint32_t parity) { wait_on(&full[s], parity, 541); };
+    while (next_item()) {
+        const int n = min(C::kTok, ntok - begin);
+        if (n <= kFew)
+            shrink_item<RT, kFew, C::kSubFew>(n, k0, k1, smem_u32(dyn), tile, empty, slot, phase,
+                                              wait_full, ok);
         else
-            shrink_group<RT, kBlockTok, C::kManyStages>(p, x, list, ntok, arow, ranks, k0, k1, dyn,
-                                                        tile);
+            shrink_item<RT, C::kTok, C::kSubMany>(n, k0, k1, smem_u32(dyn), tile, empty, slot,
+                                                  phase, wait_full, ok);
         cluster_barrier();
-        // ---- add the CTAs of the cluster in rank order: every CTA finishes a
-        // share of the (token, four ranks) entries
+        // ---- add the halves of the CTAs of the cluster in rank order: every
+        // CTA finishes a share of the (token, four ranks) entries
         const int quads = ranks / 4;
         const float sc = p.scales ? __ldg(p.scales + a) : 1.f;
-        for (int e = tid * csize + crank; e < ntok * quads; e += kShrinkWarps * 32 * csize) {
+        for (int e = tid * csize + crank; e < n * quads; e += kShrinkWarps * 32 * csize) {
             const int c = e / quads, q = e % quads;
             const float *mine = tile + c * ST + 4 * q;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < csize; ++w) {
-                const float4 v = ld_peer_f4(mine, w);
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
-            }
+            for (int w = 0; w < csize; ++w)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 v = ld_peer_f4(mine + h * (C::kTile / (int)sizeof(float)), w);
+                    s.x += v.x;
+                    s.y += v.y;
+                    s.z += v.z;
+                    s.w += v.w;
+                }
             uint32_t hi[4], lo[4];
             split_bf16(s.x * sc, hi[0], lo[0]);
             split_bf16(s.y * sc, hi[1], lo[1]);
             split_bf16(s.z * sc, hi[2], lo[2]);
             split_bf16(s.w * sc, hi[3], lo[3]);
-            p.T[(size_t)(m0 + list[c]) * (p.R / 4) + r0 / 4 + q] =
+            p.T[(size_t)(m0 + list[begin + c]) * (p.R / 4) + r0 / 4 + q] =
                 make_uint4(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16), lo[0] | (lo[1] << 16),
                            lo[2] | (lo[3] << 16));
         }
-        cluster_barrier();   // the tiles are read before the next group's
+        cluster_barrier();   // the tiles are read before the next item's
     }
 }
 
@@ -536,8 +641,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads)
             for (int s = 0; s < before; ++s)
                 copy_t(s);
         };
-        uint32_t filled = 0, b_filled = 0;       // slots with copies issued ...
-        uint32_t parity = 0, b_parity = 0;       // ... and the parity of their last fill
+        bool wrapped = false, b_wrapped = false;
         int a_last = -1;
         for (; block < block_end && ok; ++block) {
             const int m0 = block * kBlockTok;
@@ -571,8 +675,6 @@ __global__ void __launch_bounds__(Expand<S>::kThreads)
                 wait(&empty[slot], phase, 501);
                 if (!ok)
                     break;
-                filled |= 1u << slot;
-                parity = (parity & ~(1u << slot)) | ((phase ^ 1u) << slot);
                 Part &q = parts[slot];
                 if (lane < 16)
                     q.rows[lane] = mine;
@@ -606,8 +708,6 @@ __global__ void __launch_bounds__(Expand<S>::kThreads)
                     wait(&b_empty[b_slot], b_phase, 502);
                     if (!ok)
                         break;
-                    b_filled |= 1u << b_slot;
-                    b_parity = (b_parity & ~(1u << b_slot)) | ((b_phase ^ 1u) << b_slot);
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&b_full[b_slot], cols * p.R * 2);
                         bulk_g2s(dyn + C::kRing + b_slot * C::kBTile,
@@ -617,11 +717,13 @@ __global__ void __launch_bounds__(Expand<S>::kThreads)
                     if (++b_slot == C::kBStages) {
                         b_slot = 0;
                         b_phase ^= 1;
+                        b_wrapped = true;
                     }
                 }
                 if (++slot == C::kStages) {
                     slot = 0;
                     phase ^= 1;
+                    wrapped = true;
                 }
             }
         }
@@ -639,12 +741,13 @@ __global__ void __launch_bounds__(Expand<S>::kThreads)
         } else {
             // no role works on: every copy issued here has landed before the
             // CTA exits (otherwise the consumers wait for each of them)
+            // (a stage whose B was waited for in vain counts as one of these)
             for (int s = 0; s < C::kStages; ++s)
-                if (filled >> s & 1)
-                    mbar_wait(&full[s], parity >> s & 1, kWaitLimitNs);
+                if (s <= slot || wrapped)
+                    mbar_wait(&full[s], s <= slot ? phase ^ 1 : phase, kWaitLimitNs);
             for (int s = 0; s < C::kBStages; ++s)
-                if (b_filled >> s & 1)
-                    mbar_wait(&b_full[s], b_parity >> s & 1, kWaitLimitNs);
+                if (s < b_slot || b_wrapped)
+                    mbar_wait(&b_full[s], s < b_slot ? b_phase ^ 1 : b_phase, kWaitLimitNs);
         }
     } else {
         // ------------------------------------------------------- consumers
@@ -780,16 +883,28 @@ cudaError_t allow_smem(const void *fn, std::atomic<bool> (&done)[kMaxDeviceCache
 template <int RT>
 cudaError_t launch_shrink(const LoraPlan &pl, const LoraParams &p, cudaStream_t stream)
 {
+    using C = Shrink<RT>;
     const void *fn = reinterpret_cast<const void *>(&lora_shrink_kernel<RT>);
-    constexpr size_t smem = Shrink<RT>::smem;
     static std::atomic<bool> done[kMaxDeviceCache];
-    const cudaError_t e = allow_smem(fn, done, smem);
+    const cudaError_t e = allow_smem(fn, done, C::smem);
     if (e != cudaSuccess)
         return e;
+    // boxes of 64 k: a slice's ranks of A, 16 tokens of X (which only groups
+    // of more than 16 tokens use)
+    alignas(64) CUtensorMap xm{}, am{};
+    if (!encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.A, (uint64_t)p.K,
+                              (uint64_t)p.L * p.R, (uint64_t)p.K * 2, 64,
+                              (uint32_t)pl.slice_ranks, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        (p.M > kFew &&
+         !encode_tensor_map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.X, (uint64_t)p.K,
+                               (uint64_t)p.M, (uint64_t)p.ldx * 2, 64, 16,
+                               CU_TENSOR_MAP_SWIZZLE_128B)))
+        return cudaErrorInvalidValue;
     LoraParams q = p;
-    void *args[] = {&q};
+    int slices = pl.slices, ranks = pl.slice_ranks;
+    void *args[] = {&xm, &am, &q, &slices, &ranks};
     return launch_pdl_cluster(fn, dim3(pl.cluster, pl.shrink_subs, pl.blocks * pl.slices),
-                              dim3(kShrinkWarps * 32), pl.cluster, smem, stream, args);
+                              dim3(C::kThreads), pl.cluster, C::smem, stream, args);
 }
 
 template <int S>
@@ -833,20 +948,24 @@ LoraPlan plan_lora(int device, int M, int N, int K, int R)
     const int sms = device_info(device).sms;
     LoraPlan pl{};
     const long long blocks = ((long long)M + kBlockTok - 1) / kBlockTok;
-    pl.rank_tiles = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
-    pl.slices = (R + 16 * pl.rank_tiles - 1) / (16 * pl.rank_tiles);
+    // ranks above 64 in two slices
+    pl.slices = R <= 64 ? 1 : 2;
+    pl.slice_ranks = R <= 64 ? R : (R / 2 + 7) / 8 * 8;
+    pl.rank_tiles = pl.slice_ranks <= 16 ? 1 : (pl.slice_ranks <= 32 ? 2 : 4);
     pl.blocks = (int)blocks;
     const int tok = std::min(M, kBlockTok);
     // shrink: K is split over a cluster while the blocks alone leave room (two
-    // CTAs fit on an SM), with at least 32 k a warp
+    // CTAs fit on an SM; clusters of eight do not fill every SM of a GPC, so an
+    // eighth of that is left out), at least four stages of 64 k a CTA
+    const int room = 2 * sms * 7 / 8;
     pl.cluster = 1;
-    while (pl.cluster < 8 && 2 * pl.cluster * blocks * pl.slices <= 2 * sms &&
-           2 * pl.cluster * kShrinkWarps * 32 <= K)
+    while (pl.cluster < 8 && 2 * pl.cluster * blocks * pl.slices <= room &&
+           2 * pl.cluster * 256 <= K)
         pl.cluster *= 2;
     // groups of a block run side by side in what room is left: the host does
     // not know how many there are, and a share without any ends at once
     const long long shrink_ctas = blocks * pl.slices * pl.cluster;
-    pl.shrink_subs = (int)std::max<long long>(1, std::min<long long>(tok, 2 * sms / shrink_ctas));
+    pl.shrink_subs = (int)std::max<long long>(1, std::min<long long>(tok, room / shrink_ctas));
     // expand: one wave of CTAs; they share the blocks out, or, with fewer
     // blocks than that, each block's groups
     const int steps = (R + 15) / 16;
