@@ -35,7 +35,7 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kBlockTok = 64;     // tokens grouped together
+constexpr int kBlockTok = 64;     // most tokens grouped together
 constexpr int kShrinkWarps = 8;
 constexpr int kFew = 16;          // tokens of a group that takes the smaller stages
 
@@ -48,6 +48,7 @@ struct LoraParams {
     uint4 *T;                // [M][R / 4]: four hi halves, then four lo halves
     long long ldx, ldy, ldo; // row strides in elements
     int M, N, K, R, L;
+    int bt;                  // tokens of a block (at most kBlockTok)
 };
 
 // 16 bytes global -> shared, asynchronous; zeros when `in` is false.
@@ -80,30 +81,31 @@ __device__ __forceinline__ Groups group_tokens(int raw0, int raw1, int ntok, int
     Groups g;
     g.a0 = lane >= ntok ? -2 : raw0 >= 0 && raw0 < L ? raw0 : -1;
     g.a1 = lane + 32 >= ntok ? -2 : raw1 >= 0 && raw1 < L ? raw1 : -1;
-    const unsigned m0 = __match_any_sync(0xffffffffu, g.a0);
-    const unsigned lead0 = __ballot_sync(0xffffffffu, g.a0 != -2 && __ffs(m0) - 1 == lane);
-    g.of0 = m0;
-    g.of1 = 0;
-    g.leaders = lead0;
-    if (ntok > 32) {
-        const unsigned m1 = __match_any_sync(0xffffffffu, g.a1);
-        g.of1 = (u64)m1 << 32;
-        // every adapter of the upper half: which tokens of the lower have it
-        unsigned lead1 = __ballot_sync(0xffffffffu, g.a1 != -2 && __ffs(m1) - 1 == lane);
-        for (unsigned rest = lead1; rest; rest &= rest - 1) {
-            const int l = __ffs(rest) - 1;
-            const int a = __shfl_sync(0xffffffffu, g.a1, l);
-            const unsigned upper = __shfl_sync(0xffffffffu, m1, l);
-            const unsigned lower = __ballot_sync(0xffffffffu, g.a0 == a);
-            if (g.a0 == a)
-                g.of0 |= (u64)upper << 32;
-            if (g.a1 == a)
-                g.of1 |= lower;
-            if (lower)
-                lead1 &= ~(1u << l);
-        }
-        g.leaders |= (u64)lead1 << 32;
+    unsigned m00, m01 = 0, m10 = 0, m11 = 0;
+    const int a = __shfl_sync(0xffffffffu, g.a0, 0);
+    if (__all_sync(0xffffffffu, (g.a0 == a || g.a0 == -2) && (g.a1 == a || g.a1 == -2))) {
+        // one group
+        const u64 all = ntok == 64 ? ~0ull : (1ull << ntok) - 1;
+        g.of0 = g.of1 = all;
+        g.leaders = 1;
+        return g;
     }
+    m00 = __match_any_sync(0xffffffffu, g.a0);
+    m11 = ntok > 32 ? __match_any_sync(0xffffffffu, g.a1) : 0xffffffffu;
+    if (ntok > 32)
+        // the halves against each other, by independent shuffles (a loop over
+        // one half's adapters takes four times as long for many of them)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            m01 |= (unsigned)(__shfl_sync(0xffffffffu, g.a1, i) == g.a0) << i;
+            m10 |= (unsigned)(__shfl_sync(0xffffffffu, g.a0, i) == g.a1) << i;
+        }
+    g.of0 = m00 | (u64)m01 << 32;
+    g.of1 = m10 | (u64)m11 << 32;
+    const unsigned lead0 = __ballot_sync(0xffffffffu, g.a0 != -2 && __ffs(m00) - 1 == lane);
+    const unsigned lead1 =
+        __ballot_sync(0xffffffffu, g.a1 != -2 && m10 == 0 && __ffs(m11) - 1 == lane);
+    g.leaders = lead0 | (u64)lead1 << 32;
     return g;
 }
 
@@ -170,10 +172,10 @@ template <int RT>
 struct Shrink {
     static constexpr int kTok = RT == 4 ? 32 : 64;          // tokens of a group at a time
     static constexpr int sub(int rows) { return (rows + 16 * RT) * 128; }   // 64 k of tokens, ranks
-    static constexpr int kSubMany = RT == 1 ? 2 : 1, kSubFew = RT == 1 ? 4 : (RT == 2 ? 2 : 1);   // per stage
+    static constexpr int kSubMany = RT == 1 ? 2 : 1, kSubFew = RT == 1 ? 4 : 2;   // per stage
     static constexpr int kMany = kSubMany * sub(kTok), kFewStage = kSubFew * sub(kFew);
     static constexpr int kSlot = kMany > kFewStage ? kMany : kFewStage;
-    static constexpr int kSlots = RT == 1 ? 4 : 7;
+    static constexpr int kSlots = RT == 1 ? 3 : (RT == 2 ? 7 : 4);
     static constexpr int ST = 16 * RT + 4;                  // row stride of a reduced tile
     static constexpr int kTile = kTok * ST * (int)sizeof(float);
     // ring (aligned to 1024 bytes), tiles of the two halves
@@ -284,11 +286,12 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
         p.hdr->status = p.hdr->where = 0;
 
     const int block = blockIdx.z / slices, slice = blockIdx.z % slices;
-    const int m0 = block * kBlockTok, r0 = slice * slice_ranks;
+    const int m0 = block * p.bt, r0 = slice * slice_ranks;
     const int ranks = min(slice_ranks, p.R - r0);
-    const Groups grp = group_tokens(m0 + lane < p.M ? __ldcg(p.index + m0 + lane) : -1,
-                                    m0 + lane + 32 < p.M ? __ldcg(p.index + m0 + lane + 32) : -1,
-                                    min(kBlockTok, p.M - m0), p.L, lane);
+    const int btok = min(p.bt, p.M - m0);
+    const Groups grp = group_tokens(lane < btok ? __ldcg(p.index + m0 + lane) : -1,
+                                    lane + 32 < btok ? __ldcg(p.index + m0 + lane + 32) : -1, btok,
+                                    p.L, lane);
     uint8_t *list = lists[warp];
     const int crank = (int)cluster_rank(), csize = (int)cluster_size();
     const int units = (p.K + 63) / 64;
@@ -495,9 +498,9 @@ struct Expand {
     static constexpr int kThreads = (kConsumers + 1) * 32;   // + the producer
     static constexpr int kYRow = kCols * 2;
     static constexpr int kY = 16 * kYRow, kStage = kY + 16 * 64 * S;   // Y, then T rows of 4 R bytes
-    static constexpr int kStages = S == 1 ? 6 : (S == 2 ? 5 : 4);
+    static constexpr int kStages = S == 1 ? 5 : 3;
     static constexpr int kBTile = kCols * 32 * S;
-    static constexpr int kBStages = S == 1 ? 4 : (S == 8 ? 2 : 3);
+    static constexpr int kBStages = S == 1 ? 3 : 2;
     static constexpr int kRing = kStages * kStage;
     static constexpr size_t smem = (size_t)kRing + kBStages * kBTile;
     // parts that can be filled ahead of T, each with a B of its own
@@ -563,7 +566,7 @@ __device__ __forceinline__ int list_parts(const Groups &g, PartTable &tab, bool 
 }
 
 template <int S>
-__global__ void __launch_bounds__(Expand<S>::kThreads)
+__global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 : 1))
     lora_expand_kernel(const __grid_constant__ CUtensorMap y_map, const LoraParams p, int blocks,
                        int subs)
 {
@@ -612,9 +615,9 @@ __global__ void __launch_bounds__(Expand<S>::kThreads)
         // the index of the next block, ahead of its use
         int raw0, raw1;
         auto peek = [&](int b) {
-            const int m = b * kBlockTok + lane;
-            raw0 = b < block_end && m < p.M ? __ldcg(p.index + m) : -1;
-            raw1 = b < block_end && m + 32 < p.M ? __ldcg(p.index + m + 32) : -1;
+            const int m = b * p.bt + lane, end = b < block_end ? min(p.M, (b + 1) * p.bt) : 0;
+            raw0 = m < end ? __ldcg(p.index + m) : -1;
+            raw1 = m + 32 < end ? __ldcg(p.index + m + 32) : -1;
         };
         peek(block);
         const bool in_place = p.Out == p.Y;
@@ -644,16 +647,16 @@ __global__ void __launch_bounds__(Expand<S>::kThreads)
         bool wrapped = false, b_wrapped = false;
         int a_last = -1;
         for (; block < block_end && ok; ++block) {
-            const int m0 = block * kBlockTok;
+            const int m0 = block * p.bt;
             // a whole block of one adapter (a prefill chunk's) needs no list
             const int a0 = __shfl_sync(0xffffffffu, raw0, 0);
-            const bool one = m0 + kBlockTok <= p.M &&
-                             __all_sync(0xffffffffu, raw0 == a0 && raw1 == a0);
+            const bool one = m0 + p.bt <= p.M && __all_sync(0xffffffffu, raw0 == a0 &&
+                                                            (raw1 == a0 || p.bt == 32));
             int nparts;
             if (one) {
-                nparts = (a0 < 0 || a0 >= p.L) && in_place ? 0 : kBlockTok / 16;
+                nparts = (a0 < 0 || a0 >= p.L) && in_place ? 0 : p.bt / 16;
             } else {
-                const Groups grp = group_tokens(raw0, raw1, min(kBlockTok, p.M - m0), p.L, lane);
+                const Groups grp = group_tokens(raw0, raw1, min(p.bt, p.M - m0), p.L, lane);
                 __syncwarp();
                 nparts = list_parts(grp, table, in_place, lane);
             }
@@ -947,13 +950,17 @@ LoraPlan plan_lora(int device, int M, int N, int K, int R)
 {
     const int sms = device_info(device).sms;
     LoraPlan pl{};
-    const long long blocks = ((long long)M + kBlockTok - 1) / kBlockTok;
+    // blocks of 64 tokens; of 32 for up to 256, which are grouped in a third of
+    // the time (what two blocks read twice is in L2), unless one block of 64
+    // takes the batch whole
+    pl.block_tokens = M <= 32 || (M > 64 && M <= 256) ? 32 : kBlockTok;
+    const long long blocks = ((long long)M + pl.block_tokens - 1) / pl.block_tokens;
     // ranks above 64 in two slices
     pl.slices = R <= 64 ? 1 : 2;
     pl.slice_ranks = R <= 64 ? R : (R / 2 + 7) / 8 * 8;
     pl.rank_tiles = pl.slice_ranks <= 16 ? 1 : (pl.slice_ranks <= 32 ? 2 : 4);
     pl.blocks = (int)blocks;
-    const int tok = std::min(M, kBlockTok);
+    const int tok = std::min(M, pl.block_tokens);
     // shrink: K is split over a cluster while the blocks alone leave room (two
     // CTAs fit on an SM; clusters of eight do not fill every SM of a GPC, so an
     // eighth of that is left out), at least four stages of 64 k a CTA
@@ -971,7 +978,7 @@ LoraPlan plan_lora(int device, int M, int N, int K, int R)
     const int steps = (R + 15) / 16;
     pl.expand_steps = steps <= 2 ? steps : (steps <= 4 ? 4 : 8);
     pl.ntiles = (N + 255) / 256;
-    const int fit = pl.expand_steps <= 2 ? 2 : 1;   // CTAs an SM
+    const int fit = pl.expand_steps <= 2 ? 3 : (pl.expand_steps == 4 ? 2 : 1);   // CTAs an SM
     const int shares = std::max(1, fit * sms / pl.ntiles);
     if (shares <= blocks) {
         pl.expand_subs = 1;
@@ -1003,6 +1010,7 @@ cudaError_t launch_lora(const LoraPlan &pl, const LoraArgs &a, cudaStream_t stre
     p.K = a.K;
     p.R = a.R;
     p.L = a.L;
+    p.bt = pl.block_tokens;
     cudaError_t e;
     if (pl.rank_tiles == 1)
         e = launch_shrink<1>(pl, p, stream);
