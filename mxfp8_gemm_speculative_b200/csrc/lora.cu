@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
     using C = Expand<S>;
     __shared__ Part parts[C::kStages];
     __shared__ uint64_t full[C::kStages], empty[C::kStages];
-    __shared__ uint64_t b_full[C::kBStages], b_empty[C::kBStages];
+    __shared__ uint64_t b_empty[C::kBStages];
     __shared__ PartTable table;
     extern __shared__ __align__(128) uint8_t dyn[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -586,7 +586,6 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             mbar_init(&empty[i], C::kConsumers);
         }
         for (int i = 0; i < C::kBStages; ++i) {
-            mbar_init(&b_full[i], 1);
             mbar_init(&b_empty[i], C::kConsumers);
         }
         fence_barrier_init();
@@ -596,6 +595,8 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
     // by whole warps; once a wait has run out the role goes to its end
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
+        if (__all_sync(0xffffffffu, mbar_test(bar, parity)))
+            return;
         ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs));
         if (!ok && lane == 0)
             record_error(p.hdr, MXG_ERR_TIMEOUT, where);
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             for (int s = 0; s < before; ++s)
                 copy_t(s);
         };
-        bool wrapped = false, b_wrapped = false;
+        bool wrapped = false;
         int a_last = -1;
         for (; block < block_end && ok; ++block) {
             const int m0 = block * p.bt;
@@ -676,6 +677,8 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                 const bool box = run && n == 16;
                 const bool new_b = a >= 0 && a != a_last;
                 wait(&empty[slot], phase, 501);
+                if (new_b)
+                    wait(&b_empty[b_slot], b_phase, 502);
                 if (!ok)
                     break;
                 Part &q = parts[slot];
@@ -689,11 +692,24 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                 __syncwarp();
                 // a box is written whole: zeros stand for its columns past the end
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&full[slot], n * ((box ? C::kCols : cols) * 2 +
-                                                            (a < 0 ? 0 : quads * 16)));
+                    mbar_arrive_expect_tx(&full[slot],
+                                          n * ((box ? C::kCols : cols) * 2 +
+                                               (a < 0 ? 0 : quads * 16)) +
+                                              (new_b ? cols * p.R * 2 : 0));
                 __syncwarp();
                 // index, B and Y precede the shrink kernel's own wait: they are
                 // read ahead of this kernel's
+                if (new_b) {
+                    a_last = a;
+                    if (lane == 0)
+                        bulk_g2s(dyn + C::kRing + b_slot * C::kBTile,
+                                 p.B + ((size_t)a * p.N + n0) * p.R, cols * p.R * 2, &full[slot],
+                                 pol_keep);
+                    if (++b_slot == C::kBStages) {
+                        b_slot = 0;
+                        b_phase ^= 1;
+                    }
+                }
                 if (box) {
                     if (lane == 0)
                         tma_load_2d(dyn + slot * C::kStage, &y_map, n0, first, &full[slot],
@@ -706,23 +722,6 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                     copy_t(slot);
                 else
                     ++before;
-                if (new_b) {
-                    a_last = a;
-                    wait(&b_empty[b_slot], b_phase, 502);
-                    if (!ok)
-                        break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&b_full[b_slot], cols * p.R * 2);
-                        bulk_g2s(dyn + C::kRing + b_slot * C::kBTile,
-                                 p.B + ((size_t)a * p.N + n0) * p.R, cols * p.R * 2,
-                                 &b_full[b_slot], pol_keep);
-                    }
-                    if (++b_slot == C::kBStages) {
-                        b_slot = 0;
-                        b_phase ^= 1;
-                        b_wrapped = true;
-                    }
-                }
                 if (++slot == C::kStages) {
                     slot = 0;
                     phase ^= 1;
@@ -744,13 +743,9 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
         } else {
             // no role works on: every copy issued here has landed before the
             // CTA exits (otherwise the consumers wait for each of them)
-            // (a stage whose B was waited for in vain counts as one of these)
             for (int s = 0; s < C::kStages; ++s)
-                if (s <= slot || wrapped)
-                    mbar_wait(&full[s], s <= slot ? phase ^ 1 : phase, kWaitLimitNs);
-            for (int s = 0; s < C::kBStages; ++s)
-                if (s < b_slot || b_wrapped)
-                    mbar_wait(&b_full[s], s < b_slot ? b_phase ^ 1 : b_phase, kWaitLimitNs);
+                if (s < slot || wrapped)
+                    mbar_wait(&full[s], s < slot ? phase ^ 1 : phase, kWaitLimitNs);
         }
     } else {
         // ------------------------------------------------------- consumers
@@ -766,17 +761,17 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
         const bool col_in = ncol < p.N;
         const uint32_t yoff = g * C::kYRow + warp * 64 + t * 16, toff = C::kY + g * quads * 16;
         int slot = 0, b_slot = 0;
-        uint32_t phase = 0, b_phase = 0;
+        uint32_t phase = 0;
         while (true) {
             wait(&full[slot], phase, 521);
             const int4 q = *reinterpret_cast<const int4 *>(&parts[slot].ntok);
             if (!ok || q.w)   // end
                 break;
             const uint32_t st = base + slot * C::kStage;
+            const int2 row =
+                make_int2(g < q.x ? parts[slot].rows[g] : -1, g + 8 < q.x ? parts[slot].rows[g + 8] : -1);
+            const uint4 y[2] = {lds128a(st + yoff), lds128a(st + yoff + 8 * C::kYRow)};
             if (q.y) {   // new B
-                wait(&b_full[b_slot], b_phase, 522);
-                if (!ok)
-                    break;
                 // column (row of B) and ranks of this lane.  S = 1: four
                 // consecutive ranks 4 t; else eight, 32 q + 8 t, for two steps
                 const uint32_t tile = base + C::kRing + b_slot * C::kBTile;
@@ -800,17 +795,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&b_empty[b_slot]);
-                if (++b_slot == C::kBStages) {
-                    b_slot = 0;
-                    b_phase ^= 1;
-                }
             }
-            const int2 row =
-                make_int2(g < q.x ? parts[slot].rows[g] : -1, g + 8 < q.x ? parts[slot].rows[g + 8] : -1);
-            const uint4 y[2] = {lds128a(st + yoff), lds128a(st + yoff + 8 * C::kYRow)};
             uint32_t w[2][4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -849,8 +834,13 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             }
             // every lane's reads of the stage have returned: it is free
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
                 mbar_arrive(&empty[slot]);
+                if (q.y)
+                    mbar_arrive(&b_empty[b_slot]);
+            }
+            if (q.y && ++b_slot == C::kBStages)
+                b_slot = 0;
             if (col_in && row.x >= 0)
                 *reinterpret_cast<uint4 *>(p.Out + row.x * p.ldo + ncol) =
                     make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
