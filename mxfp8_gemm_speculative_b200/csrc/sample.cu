@@ -118,46 +118,46 @@ __device__ __forceinline__ float key_value(uint32_t k, uint32_t)
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// Weights of one row, round(2^kFix * exp((v - top) / T)), for finite v.
+// Weights of one row, round(2^kFix * exp((v - top) / T)), for finite v.  Nine
+// fp64 operations, which is what bounds a pass over the row.
+constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: adding it rounds to an integer
 struct Weights {
     float least;          // 48 binades below the top or lower: no weight
-    double top;
     double c;             // 64 * log2(e) / T
-    const double *table;  // 2^(j / 64)
+    double k;             // kMagic - top * c, rounded to an integer
+    const double *table;  // 2^(j / 64), less what that rounding adds
 
-    // (v - top) / T in units of 1/64 binade, its integer part in the low bits
-    __device__ __forceinline__ double scaled(float v, double &d) const
+    // (v - top) / T in units of 1/64 binade: its integer part in the low bits
+    __device__ __forceinline__ double scaled(float v) const
     {
-        constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52
-        d = (double)fmaxf(v, least) - top;
-        return fma(d, c, kMagic);
+        return fma((double)fmaxf(v, least), c, k);
     }
 
     // First-level bin: 1/16 binade of the weight, the last bin holding
     // everything from 32 binades down.  It never falls as v falls.
     __device__ __forceinline__ int bin(double m) const
     {
-        return min(-__double2loint(m) >> 2, kBins - 1);
+        return max(0, min(-__double2loint(m) >> 2, kBins - 1));
     }
 
-    __device__ __forceinline__ int bin(float v) const
+    __device__ __forceinline__ int bin(float v) const { return bin(scaled(v)); }
+
+    // 2^(f / 64) - 1 for |f| <= 1/2, by its series to the fourth order, the
+    // fifth replaced by its Chebyshev approximation x^5 = (20 h^2 x^3 - 5 h^4 x)
+    // / 16 on |x| <= h = ln2 / 128: an error of h^5 / 1920 = 2^-48.5
+    __device__ __forceinline__ static double exp_rest(double f)
     {
-        double d;
-        return bin(scaled(v, d));
+        constexpr double l = 0.69314718055994530942 / 64.0, h2 = l * l / 4.0;
+        constexpr double c1 = l * (1.0 - 5.0 * h2 * h2 / 1920.0), c2 = l * l / 2.0;
+        constexpr double c3 = l * l * l * (1.0 / 6.0 + 20.0 * h2 / 1920.0);
+        constexpr double c4 = l * l * l * l / 24.0;
+        return f * (c1 + f * (c2 + f * (c3 + f * c4)));
     }
 
-    __device__ __forceinline__ u64 weight(double m, double d) const
+    __device__ __forceinline__ u64 weight(float v, double m) const
     {
-        constexpr double kMagic = 6755399441055744.0;
         const int n = __double2loint(m);
-        const double f = fma(d, c, -(m - kMagic));
-        // 2^(f / 64) - 1 by its series: |f| <= 1/2, |f ln2 / 64| <= 0.0055,
-        // so the sixth-order term is below 2^-54
-        constexpr double l = 0.69314718055994530942 / 64.0;
-        const double q =
-            f * (l + f * (l * l / 2.0 +
-                          f * (l * l * l / 6.0 +
-                               f * (l * l * l * l / 24.0 + f * (l * l * l * l * l / 120.0)))));
+        const double q = exp_rest(fma((double)fmaxf(v, least), c, k - m));
         const double t = table[n & 63];
         const double w = fma(t, q, t);
         // times 2^(n / 64 + kFix) by the exponent field, then rounded to an
@@ -168,12 +168,7 @@ struct Weights {
         return (u64)__double_as_longlong(r) & 0xFFFFFFFFFFFFFull;
     }
 
-    __device__ __forceinline__ u64 operator()(float v) const
-    {
-        double d;
-        const double m = scaled(v, d);
-        return weight(m, d);
-    }
+    __device__ __forceinline__ u64 operator()(float v) const { return weight(v, scaled(v)); }
 };
 
 // ------------------------------------------------------------ shared memory
@@ -459,7 +454,6 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
 
     const double kLog2e = 1.4426950408889634074;
     Weights weight;
-    weight.top = (double)top;
     weight.table = s.table;
     {
         // a temperature at which the next lower float has no weight is as
@@ -467,20 +461,27 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
         const double gap = (double)top - (double)nextafterf(top, -INFINITY);
         const double t = fmax((double)temp, gap * (kLog2e / 48.0));
         weight.c = 64.0 * kLog2e / t;
+        weight.k = rint(kMagic - (double)top * weight.c);
         weight.least = fmaxf(__double2float_rd((double)top - 48.0 / kLog2e * t), -FLT_MAX);
+        // the top's own rest goes into the table, so that its weight is 1
+        if (tid < 64) {
+            const double rest = fma((double)top, weight.c, weight.k - kMagic);
+            s.table[tid] = fma(s.table[tid], Weights::exp_rest(-rest), s.table[tid]);
+        }
+        __syncthreads();
     }
 
     // ---- min-p: the lowest value that passes (the test rises with the value)
     float low = -FLT_MAX;   // -inf never passes
     if (min_p > 0.f) {
         const double cut = (double)temp * log(fmin((double)min_p, 1.0));
-        low = fmaxf(__double2float_rd(weight.top + cut), -FLT_MAX);
+        low = fmaxf(__double2float_rd((double)top + cut), -FLT_MAX);
         for (int i = 0; i < 2 && low > -FLT_MAX; ++i) {
             const float below = nextafterf(low, -INFINITY);
-            if ((double)below - weight.top >= cut)
+            if ((double)below - (double)top >= cut)
                 low = below;
         }
-        for (int i = 0; i < 3 && (double)low - weight.top < cut; ++i)
+        for (int i = 0; i < 3 && (double)low - (double)top < cut; ++i)
             low = nextafterf(low, INFINITY);
     }
 
@@ -500,11 +501,10 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
                 int bin[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    double d;
-                    const double m = weight.scaled(v[e], d);
+                    const double m = weight.scaled(v[e]);
                     bin[e] = weight.bin(m);
                     if (P)
-                        w[e] = v[e] > -INFINITY ? weight.weight(m, d) : 0;
+                        w[e] = v[e] > -INFINITY ? weight.weight(v[e], m) : 0;
                 }
                 // a warp whose entries fall into one bin (rows of equal
                 // values) adds them up first: 32 atomics on one word run one
@@ -686,17 +686,25 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
     const bool tied = cut >= low;          // ... and above the cut or among the first ties
     u64 mass = 0;
     uint32_t tie = 0;
+    // four weights side by side, where any of the four is kept
+    auto add_kept = [&](const float (&v)[4]) {
+        if (fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) < keep)
+            return;
+        u64 w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = weight(v[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = v[e] >= keep, eq = v[e] == cut;
+            mass += in && !eq ? w[e] : 0;
+            tie += in && eq;
+        }
+    };
     for (int i = b0 + 4 * lane; i < b1; i += 128) {
         float v[4];
         load4(data, i, v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (v[e] >= keep) {
-                if (v[e] == cut)
-                    ++tie;
-                else
-                    mass += weight(v[e]);
-            }
+        add_kept(v);
     }
     mass = warp_sum(mass);
     tie = __reduce_add_sync(0xffffffffu, tie);
@@ -757,14 +765,7 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
             for (int i = b0 + lane * sub; i < min(b1, b0 + (lane + 1) * sub); i += 4) {
                 float v[4];
                 load4(data, i, v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (v[e] >= keep) {
-                        if (v[e] == cut)
-                            ++tie;
-                        else
-                            mass += weight(v[e]);
-                    }
+                add_kept(v);
             }
             __syncwarp();
             part = of(mass, tie, ties_before);
