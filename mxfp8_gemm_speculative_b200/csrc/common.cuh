@@ -211,6 +211,14 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// The warp's index in its CTA, by a shuffle: the compiler then knows that it is
+// the same in all lanes, and that the branches on it keep the warp together
+// (else shuffles and votes behind them take a slow path).
+__device__ __forceinline__ int uniform_warp()
+{
+    return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+}
+
 // ------------------------------------------------- thread-block clusters
 __device__ __forceinline__ uint32_t cluster_rank()
 {

@@ -192,7 +192,7 @@ __device__ __forceinline__ void shrink_item(int ntok, int k0, int k1, uint32_t r
     using C = Shrink<RT>;
     constexpr int kHalf = kShrinkWarps / 2;
     constexpr int kPer = (ROWS / 8 + kHalf - 1) / kHalf;   // token tiles per warp
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int q = warp / kHalf, first = warp % kHalf;
     float acc[kPer][RT][4];
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
     uint8_t *dyn = dyn_raw + ((1024 - (smem_u32(dyn_raw) & 1023)) & 1023);
     float *tile = reinterpret_cast<float *>(dyn + C::kSlots * C::kSlot);   // [halves][tokens][ST]
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(&full[i], 1 + 32);   // the boxes' bytes, and every lane's own copies
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
     __shared__ uint64_t b_empty[C::kBStages];
     __shared__ PartTable table;
     extern __shared__ __align__(128) uint8_t dyn[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int n0 = blockIdx.x * C::kCols;
     const int cols = min(C::kCols, p.N - n0);
     const int quads = p.R / 4;

@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
 {
     __shared__ Shared s;
     extern __shared__ __align__(16) uint8_t dyn[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
     const int nwarps = blockDim.x >> 5;
     const uint32_t rank = cluster_rank(), ncta = cluster_size();
     const int row = blockIdx.x / ncta;
@@ -487,7 +487,8 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
 
     // ---- the cut of top-p and top-k: keep values above it, and the first
     // cut_ties in index order of those equal to it
-    const bool use_p = top_p < 1.f, use_k = top_k > 0;
+    const bool use_p = __any_sync(0xffffffffu, top_p < 1.f);
+    const bool use_k = __any_sync(0xffffffffu, top_k > 0);
     float cut = -INFINITY;
     u64 cut_ties = 0;
     if (use_p || use_k) {
@@ -555,9 +556,10 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
         // warp 0 looks for top-p's border, warp 1 for top-k's
         if (warp < 2) {
             u64 base = 0, target = warp ? (u64)max(top_k, 0) : 0;
-            int bin = kBins;   // no border: the filter is off, or keeps all
-            if (warp ? use_k : use_p)
-                bin = hist_find(s.hist[0][warp], base, target, (double)top_p, lane);
+            // no border: the filter is off, or keeps all
+            int bin = hist_find(s.hist[0][warp], base, target, (double)top_p, lane);
+            if (!(warp ? use_k : use_p))
+                bin = kBins;
             if (lane == 0)
                 s.find[warp] = Search{target, base, 0, 0, 0, bin};
         }
