@@ -42,7 +42,7 @@ typedef unsigned long long u64;
 constexpr int kBins = 512;
 constexpr int kGroups = 32;       // of 16 bins, a lane each
 constexpr int kListCap = 2048;    // entries of the border bin a CTA lists
-constexpr int kMaxCluster = 8;
+constexpr int kMaxEntries = 8 * 192 * 1024 / 4;   // fp32 entries that 8 CTAs hold
 constexpr int kMaxWarps = 32;
 constexpr int kFix = 44;          // weights are multiples of 2^-kFix
 constexpr int kSmemSlice = 192 * 1024;   // most bytes of logits a CTA holds
@@ -195,6 +195,7 @@ struct Shared {
     uint32_t wtie[kMaxWarps];    // entries equal to the cut, per warp segment
     uint32_t red[kMaxWarps];
     int listed;
+    uint32_t bound[2];           // the border bin's largest and smallest key
     // exchanged with the peers
     uint32_t top_key, first;     // largest key; first index of the maximum
     u64 mass;                    // kept mass above the cut
@@ -271,13 +272,16 @@ __device__ __forceinline__ void hist_groups(Hist &h, int thread)
 __device__ __forceinline__ int hist_find(const Hist &h, u64 &base, u64 &target, double p, int lane)
 {
     const uint32_t n = cluster_size();
-    u64 part[kMaxCluster], v = 0;
+    u64 v = 0;
+    for (uint32_t c0 = 0; c0 < n; c0 += 8) {
+        u64 part[8];
 #pragma unroll
-    for (uint32_t c = 0; c < kMaxCluster; ++c)
-        part[c] = c < n ? ld_peer64(&h.group[lane], c) : 0;
+        for (uint32_t c = 0; c < 8; ++c)
+            part[c] = c0 + c < n ? ld_peer64(&h.group[lane], c0 + c) : 0;
 #pragma unroll
-    for (uint32_t c = 0; c < kMaxCluster; ++c)
-        v += part[c];
+        for (uint32_t c = 0; c < 8; ++c)
+            v += part[c];
+    }
     u64 incl = base + warp_scan(v, lane);
     if (target == 0)
         target = max(1ull, (u64)ceil(p * (double)(__shfl_sync(0xffffffffu, incl, 31) - base)));
@@ -289,17 +293,19 @@ __device__ __forceinline__ int hist_find(const Hist &h, u64 &base, u64 &target, 
     // 16 bins, the peers shared between the halves of the warp
     constexpr int kPer = kBins / kGroups;
     const int i = g * kPer + lane % kPer;
-    uint32_t lo[kMaxCluster / 2], hi[kMaxCluster / 2];
-#pragma unroll
-    for (uint32_t c = 0; c < kMaxCluster / 2; ++c) {
-        const uint32_t peer = 2 * c + lane / kPer;
-        lo[c] = peer < n ? ld_peer(&h.lo[i], peer) : 0;
-        hi[c] = peer < n ? ld_peer(&h.hi[i], peer) : 0;
-    }
     v = 0;
+    for (uint32_t c0 = 0; c0 < n; c0 += 8) {
+        uint32_t lo[4], hi[4];
 #pragma unroll
-    for (uint32_t c = 0; c < kMaxCluster / 2; ++c)
-        v += (u64)lo[c] + ((u64)hi[c] << 32);
+        for (uint32_t c = 0; c < 4; ++c) {
+            const uint32_t peer = c0 + 2 * c + lane / kPer;
+            lo[c] = peer < n ? ld_peer(&h.lo[i], peer) : 0;
+            hi[c] = peer < n ? ld_peer(&h.hi[i], peer) : 0;
+        }
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c)
+            v += (u64)lo[c] + ((u64)hi[c] << 32);
+    }
     v += __shfl_xor_sync(0xffffffffu, v, kPer);
     if (lane >= kPer)
         v = 0;
@@ -569,18 +575,22 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
         const int bin = min(s.find[0].bin, s.find[1].bin);
         if (bin < kBins) {
             const bool do_p = s.find[0].bin == bin, do_k = s.find[1].bin == bin;
-            // the bin's keys are kl .. kh
-            const uint32_t k_min = key_of(-FLT_MAX, T(0)), k_top = key_of(top, T(0));
-            auto key_bin = [&](uint32_t k) { return weight.bin(key_value(k, T(0))); };
-            const uint32_t kh = bin == 0 ? k_top
-                                         : last_key(k_min, k_top, lane,
-                                                    [&](uint32_t k) { return key_bin(k) >= bin; });
-            uint32_t kl = k_min;
-            if (key_bin(k_min) > bin)
-                kl = last_key(k_min, kh, lane, [&](uint32_t k) { return key_bin(k) > bin; }) + 1;
+            // the bin's keys are kl .. kh: a warp for each end
+            if (warp < 2) {
+                const uint32_t k_min = key_of(-FLT_MAX, T(0)), k_top = key_of(top, T(0));
+                // the last key whose bin is at least `bin` (kh), or above it (kl - 1)
+                const int least = bin + warp;
+                auto yes = [&](uint32_t k) { return weight.bin(key_value(k, T(0))) >= least; };
+                uint32_t k = last_key(k_min, k_top, lane, yes);
+                if (warp == 1)
+                    k = yes(k_min) ? k + 1 : k_min;
+                if (lane == 0)
+                    s.bound[warp] = k;
+            }
+            __syncthreads();
+            const uint32_t kh = s.bound[0], kl = s.bound[1];
             const float vl = key_value(kl, T(0)), vh = key_value(kh, T(0));
             const int sh0 = max(0, 32 - __clz(kh - kl) - 9);   // bins of 2^sh keys from kh down
-            __syncthreads();
             if (tid < 2) {
                 s.find[tid].l = kl;
                 s.find[tid].r = kh;
@@ -803,6 +813,62 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
     cluster_wait();
 }
 
+// The kernel's attributes, set once per device.
+template <typename T>
+cudaError_t prepare_kernel(int dev)
+{
+    const void *fn = reinterpret_cast<const void *>(&sample_kernel<T>);
+    static std::atomic<bool> done[kMaxDeviceCache];
+    if (done[dev].load(std::memory_order_acquire))
+        return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmemSlice + kSlack * (int)sizeof(T));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+        done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+// Clusters of 16 CTAs that the device runs at the same time (0 where it takes
+// none), asked once per device.
+template <typename T>
+int wide_clusters_of(int dev)
+{
+    static std::atomic<int> known[kMaxDeviceCache];   // plus one
+    if (dev < 0 || dev >= kMaxDeviceCache)
+        return 0;
+    int n = known[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        int got = 0;
+        if (prepare_kernel<T>(dev) == cudaSuccess) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(16);
+            cfg.blockDim = dim3(1024);
+            cfg.dynamicSmemBytes = (size_t)(kMaxEntries / 16 + kSlack) * sizeof(T);
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 16;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&got, &sample_kernel<T>, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                got = 0;
+            }
+        }
+        n = 1 + std::max(0, got);
+        known[dev].store(n, std::memory_order_release);
+    }
+    return n - 1;
+}
+
+int wide_clusters(int dev, bool fp32)
+{
+    return fp32 ? wide_clusters_of<uint32_t>(dev) : wide_clusters_of<uint16_t>(dev);
+}
+
 template <typename T>
 cudaError_t launch_typed(const SamplePlan &pl, const SampleParams &p, cudaStream_t stream)
 {
@@ -813,14 +879,8 @@ cudaError_t launch_typed(const SamplePlan &pl, const SampleParams &p, cudaStream
         return e;
     if (dev < 0 || dev >= kMaxDeviceCache)
         return cudaErrorInvalidDevice;
-    static std::atomic<bool> done[kMaxDeviceCache];
-    if (!done[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmemSlice + kSlack * (int)sizeof(T));
-        if (e != cudaSuccess)
-            return e;
-        done[dev].store(true, std::memory_order_release);
-    }
+    if ((e = prepare_kernel<T>(dev)) != cudaSuccess)
+        return e;
     SampleParams q = p;
     void *args[] = {&q};
     return launch_pdl_cluster(fn, dim3((unsigned)p.M * pl.cluster), dim3(pl.threads), pl.cluster,
@@ -833,20 +893,22 @@ bool sample_shape_ok(int M, int V)
 {
     // a row fits the shared memory of its cluster as fp32; rows times
     // clusters are a grid dimension
-    return M >= 1 && M <= (1 << 27) && V >= 1 && V <= kMaxCluster * kSmemSlice / 4;
+    return M >= 1 && M <= (1 << 27) && V >= 1 && V <= kMaxEntries;
 }
 
 SamplePlan plan_sample(int device, int M, int V, bool fp32)
 {
     const int size = fp32 ? 4 : 2;
     SamplePlan pl{};
-    // a CTA per 4096 entries at least while that leaves SMs idle
+    // a CTA per 4096 entries at least while that leaves SMs idle.  Sixteen CTAs
+    // take a GPC, of which a device has one for about 18 SMs
     const int sms = device_info(device).sms;
     pl.cluster = 1;
-    while (pl.cluster < kMaxCluster &&
-           ((V > 4096 * pl.cluster && (long long)M * pl.cluster * 2 <= sms) ||
-            (long long)(V + pl.cluster - 1) / pl.cluster * size > 72 * 1024))
+    while (pl.cluster < 8 && ((V > 4096 * pl.cluster && (long long)M * pl.cluster * 2 <= sms) ||
+                              (long long)(V + pl.cluster - 1) / pl.cluster * size > 72 * 1024))
         pl.cluster *= 2;
+    if (pl.cluster == 8 && V > 8 * 4096 && M <= wide_clusters(device, fp32))
+        pl.cluster = 16;
     pl.per = ((V + pl.cluster - 1) / pl.cluster + 7) / 8 * 8;
     pl.threads = (long long)M * pl.cluster <= sms ? 1024 : 512;
     pl.smem = ((size_t)pl.per + kSlack) * size;   // whole groups of 128 slots, and the skew
