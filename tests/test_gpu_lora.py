@@ -243,3 +243,51 @@ def test_lora_prepared_call(mxg):
     x.copy_(torch.flip(x, [0]))
     call()
     check(out, x, a, b, index, y, s)
+
+
+@pytest.mark.parametrize("R", [16, 32, 64, 128])
+@pytest.mark.parametrize("M,K,N,L", [(700, 520, 8712, 150),     # many parts per CTA, few CTAs a tile
+                                     (64, 4104, 264, 80),       # several groups per cluster of eight
+                                     (200, 4096, 512, 3)])      # groups above 16 tokens, scattered
+def test_lora_scattered_batches(mxg, M, K, N, L, R):
+    x, a, b, index, y, s = case(M, K, N, R, L, seed=M + R)
+    check(mxg.lora_add(x, a, b, index, y, scales=s), x, a, b, index, y, s)
+    y2 = y.clone()
+    assert torch.equal(mxg.lora_add(x, a, b, index, y2, scales=s, out=y2),
+                       mxg.lora_add(x, a, b, index, y, scales=s))
+
+
+@pytest.mark.parametrize("R", [16, 64])
+def test_lora_runs_at_every_offset(mxg, R):
+    """Runs of one adapter that start and end anywhere in the blocks, some as
+    long as a box of 16 tokens, between tokens without an adapter."""
+    lengths = [16, 1, 17, 15, 64, 3, 33, 48, 16, 32, 31, 70, 16, 5, 128]
+    index = torch.cat([torch.full((n,), i % 4 - 1) for i, n in enumerate(lengths)])
+    x, a, b, index, y, s = case(len(index), 328, 520, R, 3, seed=R, index=index)
+    check(mxg.lora_add(x, a, b, index, y, scales=s), x, a, b, index, y, s)
+
+
+def test_lora_workspace_and_status_word(mxg):
+    """A workspace of the caller's, full of anything; its status word is
+    cleared; a workspace that is too small is refused before a launch."""
+    x, a, b, index, y, s = case(40, 512, 256, 24, 4, seed=6)
+    need = mxg.lora_workspace_bytes(40, 256, 512, 24)
+    ws = torch.full((need + 64,), 0x5A, dtype=torch.uint8, device=DEV)
+    got = mxg.lora_add(x, a, b, index, y, scales=s, workspace_buf=ws)
+    check(got, x, a, b, index, y, s)
+    assert mxg.mxg_workspace_status(ws) == 0
+    assert (ws[need:] == 0x5A).all()
+    with pytest.raises(mxg.MxgError):
+        mxg.lora_add(x, a, b, index, y, workspace_buf=ws[: need - 16])
+
+
+def test_lora_calls_at_once_on_two_streams(mxg):
+    cases = [case(33, 2048, 2048, 16, 8, seed=i) for i in (20, 21)]
+    want = [mxg.lora_add(*c[:5], scales=c[5]) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [mxg.lora_add(*c[:5], scales=c[5], stream=st) for c, st in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
