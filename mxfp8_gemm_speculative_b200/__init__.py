@@ -162,7 +162,9 @@ def _dev_call(device, what: str, fn, *args, stream=None) -> None:
     """fn(*args, stream handle) with ``device`` current; raises on a nonzero
     status."""
     with _on_device(device):
-        _check(fn(*args, _stream(stream, device)), what)
+        status = fn(*args, _stream(stream, device))
+    if status != MXG_OK:
+        raise MxgError(status, what)
 
 
 def _need(t: torch.Tensor, dtype, name: str) -> None:
@@ -711,9 +713,12 @@ def bf16_gemm_small(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None =
 # ------------------------------------------------------- low-rank adapters
 # Calls of a few microseconds: the checks below take the pointer of an
 # argument that is in order at once, and look for what is wrong only otherwise.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
 def _dense(t: torch.Tensor, dtype, shape, device, name: str) -> int:
     """The pointer of a contiguous tensor of this type and shape."""
-    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+    if not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         _need_shape(t, shape, name)
@@ -737,11 +742,11 @@ def _empty_as(t: torch.Tensor, dtype, stream) -> torch.Tensor:
 
 def _need_rows(t: torch.Tensor, M: int, N: int, device, name: str) -> int:
     """The row stride of a bf16 [M][N] whose rows are contiguous."""
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.shape != (M, N):
-        raise ValueError(f"{name} must be [{M}][{N}], got {list(t.shape)}")
-    if t.device != device:
+    if not (t.dtype is _BF16 and t.shape == (M, N) and t.device == device):
+        if t.dtype != _BF16:
+            raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+        if t.shape != (M, N):
+            raise ValueError(f"{name} must be [{M}][{N}], got {list(t.shape)}")
         _same_device(t, device, name)
     ld, one = t.stride()
     if one != 1 and N > 1:
@@ -769,27 +774,28 @@ def _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream):
     """The arguments of the C call, and the tensors behind them."""
     dev = x.device
     _need_cuda(x, "x")
-    if a.dim() != 3 or b.dim() != 3:
+    shape_a, shape_b, shape_x = a.shape, b.shape, x.shape
+    if len(shape_a) != 3 or len(shape_b) != 3:
         raise ValueError("a must be [L][R][K] and b [L][N][R]")
-    L, R, K = a.shape
-    N = b.shape[1]
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M][{K}], got {list(x.shape)}")
-    M = x.shape[0]
-    pa = _dense(a, torch.bfloat16, (L, R, K), dev, "a")
-    pb = _dense(b, torch.bfloat16, (L, N, R), dev, "b")
-    pi = _dense(index, torch.int32, (M,), dev, "index")
-    ps = None if scales is None else _dense(scales, torch.float32, (L,), dev, "scales")
+    L, R, K = shape_a
+    N = shape_b[1]
+    if len(shape_x) != 2:
+        raise ValueError(f"x must be [M][{K}], got {list(shape_x)}")
+    M = shape_x[0]
+    pa = _dense(a, _BF16, shape_a, dev, "a")
+    pb = _dense(b, _BF16, (L, N, R), dev, "b")
+    pi = _dense(index, _I32, (M,), dev, "index")
+    ps = None if scales is None else _dense(scales, _F32, (L,), dev, "scales")
     ldx = _need_rows(x, M, K, dev, "x")
     ldy = _need_rows(y, M, N, dev, "y")
     need = _lora_bytes(M, N, K, R)
     if need == 0:
         raise MxgError(MXG_ERR_UNSUPPORTED_SHAPE, "lora_add")
     if out is None:
-        if y.is_contiguous():
-            out = _empty_as(y, torch.bfloat16, stream)
+        if ldy == N and y.is_contiguous():
+            out = _empty_as(y, _BF16, stream)
         else:
-            out = _empty((M, N), torch.bfloat16, dev, stream)
+            out = _empty((M, N), _BF16, dev, stream)
         ldo = N
     else:
         ldo = _need_rows(out, M, N, dev, "out")
@@ -800,14 +806,15 @@ def _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream):
         # this call's own, from the stream's pool: calls captured into
         # different graphs never share it
         if stream is None:
-            ws = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev)
+            ws = torch.empty_strided((need,), (1,), dtype=_U8, device=dev)
         else:
-            ws = _empty((need,), torch.uint8, dev, stream)
+            ws = _empty((need,), _U8, dev, stream)
     else:
         ws = workspace_buf
         _need_ws(ws, dev)
+        need = ws.numel()
     args = (x.data_ptr(), ldx, pa, pb, ps, pi, y.data_ptr(), ldy, out.data_ptr(), ldo, M, N, K, R,
-            L, ws.data_ptr(), ws.numel())
+            L, ws.data_ptr(), need)
     return args, out, (x, a, b, scales, index, y, out, ws, stream)
 
 
@@ -860,8 +867,7 @@ def _sample_args(logits, u, temperature, top_k, top_p, min_p, tokens, probs, str
         ld = V
     if u is None:
         raise ValueError("u must be given: one random number per row")
-    shape = (M,)
-    f32, i32 = torch.float32, torch.int32
+    shape, f32, i32 = (M,), _F32, _I32
     pu = _dense(u, f32, shape, dev, "u")
     pt = None if temperature is None else _dense(temperature, f32, shape, dev, "temperature")
     pk = None if top_k is None else _dense(top_k, i32, shape, dev, "top_k")
