@@ -108,8 +108,7 @@ cudaError_t launch_bf16_small(const SmallPlan &plan, const void *X, const void *
 
 // ------------------------------------------------------ low-rank adapters
 struct LoraPlan {
-    int block_tokens;     // tokens grouped by adapter together
-    int blocks;           // blocks of so many
+    int blocks;           // blocks of 64 tokens
     int slices;           // rank slices (shrink)
     int slice_ranks;      // ranks of a slice (the last may have fewer)
     int rank_tiles;       // 16-rank tiles of the shrink variant (1, 2, 4)

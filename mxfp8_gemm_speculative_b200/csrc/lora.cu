@@ -20,9 +20,8 @@
 //            MMAs of the expand kernel);
 //   expand   Out = Y + T B^T, summed in fp32 and rounded once.
 //
-// Tokens come in any order.  Both kernels take blocks of 64 (small batches 32)
-// consecutive tokens and group a block's tokens by adapter with warp
-// instructions (no sort kernel, no host plan, nothing read back), so an
+// Tokens come in any order.  Both kernels take blocks of 64 consecutive tokens
+// and group a block's tokens by adapter with warp instructions (no sort kernel, no host plan, nothing read back), so an
 // adapter is read once per block that uses it and once in all for up to 64
 // tokens.
 //
@@ -42,7 +41,7 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kBlockTok = 64;     // most tokens grouped together
+constexpr int kBlockTok = 64;     // tokens grouped together
 constexpr int kShrinkWarps = 8;
 constexpr int kFew = 16;          // tokens of a group that takes the smaller stages
 
@@ -55,7 +54,6 @@ struct LoraParams {
     uint4 *T;                // [M][R / 4]: four hi halves, then four lo halves
     long long ldx, ldy, ldo; // row strides in elements
     int M, N, K, R, L;
-    int bt;                  // tokens of a block (at most kBlockTok)
 };
 
 // 16 bytes global -> shared, asynchronous; zeros when `in` is false.
@@ -293,9 +291,9 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
         p.hdr->status = p.hdr->where = 0;
 
     const int block = blockIdx.z / slices, slice = blockIdx.z % slices;
-    const int m0 = block * p.bt, r0 = slice * slice_ranks;
+    const int m0 = block * kBlockTok, r0 = slice * slice_ranks;
     const int ranks = min(slice_ranks, p.R - r0);
-    const int btok = min(p.bt, p.M - m0);
+    const int btok = min(kBlockTok, p.M - m0);
     const Groups grp = group_tokens(lane < btok ? __ldcg(p.index + m0 + lane) : -1,
                                     lane + 32 < btok ? __ldcg(p.index + m0 + lane + 32) : -1, btok,
                                     p.L, lane);
@@ -623,7 +621,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
         // the index of the next block, ahead of its use
         int raw0, raw1;
         auto peek = [&](int b) {
-            const int m = b * p.bt + lane, end = b < block_end ? min(p.M, (b + 1) * p.bt) : 0;
+            const int m = b * kBlockTok + lane, end = b < block_end ? min(p.M, (b + 1) * kBlockTok) : 0;
             raw0 = m < end ? __ldcg(p.index + m) : -1;
             raw1 = m + 32 < end ? __ldcg(p.index + m + 32) : -1;
         };
@@ -655,16 +653,16 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
         bool wrapped = false;
         int a_last = -1;
         for (; block < block_end && ok; ++block) {
-            const int m0 = block * p.bt;
+            const int m0 = block * kBlockTok;
             // a whole block of one adapter (a prefill chunk's) needs no list
             const int a0 = __shfl_sync(0xffffffffu, raw0, 0);
-            const bool one = m0 + p.bt <= p.M && __all_sync(0xffffffffu, raw0 == a0 &&
-                                                            (raw1 == a0 || p.bt == 32));
+            const bool one =
+                m0 + kBlockTok <= p.M && __all_sync(0xffffffffu, raw0 == a0 && raw1 == a0);
             int nparts;
             if (one) {
-                nparts = (a0 < 0 || a0 >= p.L) && in_place ? 0 : p.bt / 16;
+                nparts = (a0 < 0 || a0 >= p.L) && in_place ? 0 : kBlockTok / 16;
             } else {
-                const Groups grp = group_tokens(raw0, raw1, min(p.bt, p.M - m0), p.L, lane);
+                const Groups grp = group_tokens(raw0, raw1, min(kBlockTok, p.M - m0), p.L, lane);
                 __syncwarp();
                 nparts = list_parts(grp, table, in_place, lane);
             }
@@ -947,17 +945,13 @@ LoraPlan plan_lora(int device, int M, int N, int K, int R)
 {
     const int sms = device_info(device).sms;
     LoraPlan pl{};
-    // blocks of 64 tokens; of 32 for up to 256, which are grouped in a third of
-    // the time (what two blocks read twice is in L2), unless one block of 64
-    // takes the batch whole
-    pl.block_tokens = M <= 32 || (M > 64 && M <= 256) ? 32 : kBlockTok;
-    const long long blocks = ((long long)M + pl.block_tokens - 1) / pl.block_tokens;
+    const long long blocks = ((long long)M + kBlockTok - 1) / kBlockTok;
     // ranks above 64 in two slices
     pl.slices = R <= 64 ? 1 : 2;
     pl.slice_ranks = R <= 64 ? R : (R / 2 + 7) / 8 * 8;
     pl.rank_tiles = pl.slice_ranks <= 16 ? 1 : (pl.slice_ranks <= 32 ? 2 : 4);
     pl.blocks = (int)blocks;
-    const int tok = std::min(M, pl.block_tokens);
+    const int tok = std::min(M, kBlockTok);
     // shrink: K is split over a cluster while the blocks alone leave room (two
     // CTAs fit on an SM; clusters of eight do not fill every SM of a GPC, so an
     // eighth of that is left out), at least four stages of 64 k a CTA
@@ -1007,7 +1001,6 @@ cudaError_t launch_lora(const LoraPlan &pl, const LoraArgs &a, cudaStream_t stre
     p.K = a.K;
     p.R = a.R;
     p.L = a.L;
-    p.bt = pl.block_tokens;
     cudaError_t e;
     if (pl.rank_tiles == 1)
         e = launch_shrink<1>(pl, p, stream);
