@@ -590,9 +590,8 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], C::kConsumers);
         }
-        for (int i = 0; i < C::kBStages; ++i) {
+        for (int i = 0; i < C::kBStages; ++i)
             mbar_init(&b_empty[i], C::kConsumers);
-        }
         fence_barrier_init();
     }
     __syncthreads();
@@ -600,7 +599,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
     // by whole warps; once a wait has run out the role goes to its end
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
-        if (__all_sync(0xffffffffu, mbar_test(bar, parity)))
+        if (!ok || __all_sync(0xffffffffu, mbar_test(bar, parity)))
             return;
         ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs));
         if (!ok && lane == 0)
@@ -621,7 +620,8 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
         // the index of the next block, ahead of its use
         int raw0, raw1;
         auto peek = [&](int b) {
-            const int m = b * kBlockTok + lane, end = b < block_end ? min(p.M, (b + 1) * kBlockTok) : 0;
+            const int m = b * kBlockTok + lane;
+            const int end = b < block_end ? min(p.M, (b + 1) * kBlockTok) : 0;
             raw0 = m < end ? __ldcg(p.index + m) : -1;
             raw1 = m + 32 < end ? __ldcg(p.index + m + 32) : -1;
         };
@@ -773,8 +773,8 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             if (!ok || q.w)   // end
                 break;
             const uint32_t st = base + slot * C::kStage;
-            const int2 row =
-                make_int2(g < q.x ? parts[slot].rows[g] : -1, g + 8 < q.x ? parts[slot].rows[g + 8] : -1);
+            const int2 row = make_int2(g < q.x ? parts[slot].rows[g] : -1,
+                                       g + 8 < q.x ? parts[slot].rows[g + 8] : -1);
             const uint4 y[2] = {lds128a(st + yoff), lds128a(st + yoff + 8 * C::kYRow)};
             if (q.y) {   // new B
                 // column (row of B) and ranks of this lane.  S = 1: four
