@@ -21,9 +21,9 @@
 //   expand   Out = Y + T B^T, summed in fp32 and rounded once.
 //
 // Tokens come in any order.  Both kernels take blocks of 64 consecutive tokens
-// and group a block's tokens by adapter with warp instructions (no sort kernel, no host plan, nothing read back), so an
-// adapter is read once per block that uses it and once in all for up to 64
-// tokens.
+// and group a block's tokens by adapter with warp instructions (no sort
+// kernel, no host plan, nothing read back), so an adapter is read once per
+// block that uses it and once in all for up to 64 tokens.
 //
 // Measured (B200, graph of calls over rotating buffers): 8192 tokens,
 // 5120 -> 17408, R = 16: 117 us for 658 MB (5.6 TB/s; shrink 24, expand 94);
