@@ -590,7 +590,7 @@ int sample_logits(const void *logits, int dtype, long long ld, int M, int V, con
     const int dev = current_device();
     if (dev < 0)
         return MXG_ERR_CUDA;
-    const SamplePlan pl = plan_sample(dev, M, V, fp32);
+    const SamplePlan pl = plan_sample(dev, M, V, fp32, top_p || top_k);
     const SampleArgs a{logits, fp32, ld, M, V, u, temperature, top_p, min_p, top_k, tokens, probs};
     return to_status(launch_sample(pl, a, stream));
 }

@@ -134,6 +134,7 @@ cudaError_t launch_lora(const LoraPlan &plan, const LoraArgs &args, cudaStream_t
 
 // --------------------------------------------------------------- sampling
 struct SamplePlan {
+    bool table;           // a CTA per row that counts values; the rest unused
     int cluster;          // CTAs per row
     int per;              // entries per CTA
     int threads;
@@ -150,7 +151,8 @@ struct SampleArgs {
     float *probs;
 };
 bool sample_shape_ok(int M, int V);
-SamplePlan plan_sample(int device, int M, int V, bool fp32);   // of a shape that is ok
+SamplePlan plan_sample(int device, int M, int V, bool fp32,
+                       bool filtered);   // of a shape that is ok; top-p or top-k given
 cudaError_t launch_sample(const SamplePlan &plan, const SampleArgs &args, cudaStream_t stream);
 
 // ------------------------------------------------------------ weight tools
