@@ -933,12 +933,10 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)   // of two bf1
     asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ __nv_bfloat162 exp2_approx(__nv_bfloat162 x)
+__device__ __forceinline__ float exp2_approx(float x)
 {
-    __nv_bfloat162 y;
-    asm("ex2.approx.ftz.bf16x2 %0, %1;"
-        : "=r"(reinterpret_cast<uint32_t &>(y))
-        : "r"(reinterpret_cast<const uint32_t &>(x)));
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t equal2(uint32_t a, uint32_t b)   // ones where equal
@@ -1079,8 +1077,9 @@ __global__ void __launch_bounds__(kTableThreads, 1) sample_table_kernel(const Sa
         });
     };
     if (!greedy) {
-        // and, for the order of the second pass, a rough mass per batch, in
-        // bf16 and relative to the largest of the first 256 entries
+        // and, for the order of the second pass, a rough mass per batch: the
+        // largest weight of every eight entries, in fp32 and relative to the
+        // largest of the first 256
         const uint4 v = lane < vecs ? load(lane) : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u,
                                                                0xFF80FF80u);
         const uint32_t ref2 = max2(max2(v.x, v.y), max2(v.z, v.w));
@@ -1089,17 +1088,13 @@ __global__ void __launch_bounds__(kTableThreads, 1) sample_table_kernel(const Sa
                               key_of(fmaxf(__uint_as_float(ref2 << 16),
                                            __uint_as_float(ref2 & 0xFFFF0000u)), 0u)), 0u);
         const float c = (float)kLog2e / temp;
-        const __nv_bfloat162 c2 = __float2bfloat162_rn(c);
-        const __nv_bfloat162 d2 = __float2bfloat162_rn(fabsf(ref) < INFINITY ? -ref * c : 0.f);
+        const float d = fabsf(ref) < INFINITY ? -ref * c : 0.f;
         for (int b = 0; b * 4 * kTableThreads < vecs; ++b) {
             float g = 0.f;
             for_batch(b, [&](int, const uint32_t (&w)[4]) {
-                __nv_bfloat162 e[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    e[j] = exp2_approx(__hfma2(reinterpret_cast<const __nv_bfloat162 &>(w[j]), c2, d2));
-                const float2 f = __bfloat1622float2(__hadd2(__hadd2(e[0], e[1]), __hadd2(e[2], e[3])));
-                g += f.x + f.y;
+                const uint32_t top2 = max2(max2(w[0], w[1]), max2(w[2], w[3]));
+                g += exp2_approx(fmaf(fmaxf(__uint_as_float(top2 << 16),
+                                            __uint_as_float(top2 & 0xFFFF0000u)), c, d));
                 count(w);
             });
 #pragma unroll
