@@ -281,6 +281,149 @@ def test_sample_reproducible_whatever_the_batch(mxg):
         assert torch.equal(mxg.sample_logits(logits, u, top_k=k, top_p=p)[0], want[0])
 
 
+def alone(mxg, logits, u, t=None, k=None, p=None, q=None):
+    """Every row in a call of its own: clusters, which the tests above hold to
+    the definition."""
+    out = [mxg.sample_logits(logits[m:m + 1], u[m:m + 1],
+                             *[None if v is None else v[m:m + 1] for v in (t, k, p, q)])
+           for m in range(len(u))]
+    return torch.cat([a for a, _ in out]), torch.cat([b for _, b in out])
+
+
+def both(mxg, logits, u, *filters):
+    got, want = mxg.sample_logits(logits, u, *filters), alone(mxg, logits, u, *filters)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    return got[0]
+
+
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 255, 257, 2000, 16384, 32003, 40001, 131072, 248320])
+def test_sample_batches_of_bf16_rows(mxg, V):
+    """A batch that gives every row an SM counts values; the tokens and
+    probabilities are those of the rows by themselves, bit by bit."""
+    M = 40 if V > 40000 else 64
+    rng = np.random.default_rng(V)
+    logits = rows(M, V, torch.bfloat16, V)
+    u = torch.tensor(uniform(M, V), device=DEV)
+    u[0], u[1], u[2] = 0.0, 0.99999994, float("nan")
+    t = torch.tensor(rng.choice(np.float32([0.0, 0.5, 1.0, 1.5, 1e-6, 1e6]), M), device=DEV)
+    k = torch.tensor(rng.choice(np.int32([0, 1, 50, 1000, V, 2 ** 31 - 1]), M), device=DEV)
+    p = torch.tensor(rng.choice(np.float32([1.0, 0.0, 0.3, 0.9, 0.999, 0.99999994]), M), device=DEV)
+    q = torch.tensor(rng.choice(np.float32([0.0, 1e-30, 0.02, 0.9, 1.0]), M), device=DEV)
+    both(mxg, logits, u, t, k, p, q)
+    both(mxg, logits, u, None, k)
+    both(mxg, logits, u, t, None, p)
+    off = torch.ones(M, device=DEV)
+    both(mxg, logits, u, t, None, off, q)          # the filters given but off
+    both(mxg, logits, u, None, torch.zeros(M, dtype=torch.int32, device=DEV))
+
+
+def test_sample_batches_of_masked_and_special_rows(mxg):
+    M, V = 48, 2051
+    logits = rows(M, V, torch.bfloat16, 9)
+    low, nan = torch.finfo(torch.bfloat16).min, float("nan")
+    logits[0] = -INF
+    logits[1] = nan
+    logits[2, 1:] = -INF
+    logits[3, :-1] = -INF
+    logits[4, ::2] = -INF
+    logits[5, 100:] = nan
+    logits[6, [7, 1999]] = INF
+    logits[7] = low
+    logits[8, 5:] = low
+    logits[9] = 0.0
+    logits[9, ::3] = -0.0
+    logits[10] = torch.finfo(torch.bfloat16).max
+    logits[10, 3] = low
+    logits[11, 17] = nan
+    logits[12] = 0.0
+    logits[13] = -0.0
+    logits[14, ::2], logits[14, 1::2] = 1e-40, -1e-40       # below the normal numbers
+    logits[15].view(torch.int16)[5:900] = -1                # NaN with its sign set
+    logits[16].view(torch.int16)[5:900] = 0x7FFF
+    logits[17] = INF
+    logits[18, ::2], logits[18, 1::2] = INF, -INF
+    logits[19] = -1e-40
+    logits[19, 5] = 0.0
+    logits[20, :] = -1.0
+    logits[20, 2050] = -0.99609375
+    u = torch.tensor(uniform(M, 4), device=DEV)
+
+    def of(v, dtype=torch.float32):
+        return torch.full((M,), v, dtype=dtype, device=DEV)
+    got = both(mxg, logits, u, None, of(0, torch.int32))
+    assert got[:4].tolist() == [-1, -1, 0, V - 1] and int(got[6]) in (7, 1999)
+    check(mxg, logits, u.cpu().numpy(), 0.7, 50, 0.9, 0.01)
+    for q in (0.0, 1e-38, 0.3, 0.9962, 1.0):
+        both(mxg, logits, u, of(1.0), of(700, torch.int32), None, of(q))
+        both(mxg, logits, u, of(0.6), None, of(0.9), of(q))
+    both(mxg, logits, u, of(0.0), of(5, torch.int32))
+    both(mxg, logits, u, of(1e30), None, of(0.5))
+
+
+@pytest.mark.parametrize("V", [66000, 140000, 300000])
+def test_sample_batches_of_values_that_occur_often(mxg, V):
+    """More than 65535 entries of one value, of either sign, with borders at,
+    above and below them."""
+    M = 42
+    g = torch.Generator(device=DEV)
+    g.manual_seed(V)
+    logits = rows(M, V, torch.bfloat16, V)
+    logits[:6] = -2.0                                       # all of a row
+    logits[6:12] = 0.5
+    few = torch.rand(V, generator=g, device=DEV) < 0.002
+    logits[12:18] = torch.where(few, logits[12:18], -2.0)   # nearly all of it
+    logits[18:24] = torch.where(few, logits[18:24], 0.5)
+    logits[24:30, 65537:] = -1.0
+    logits[24:30, :65537] = 1.0                             # the same magnitude
+    logits[30:36, :65536] = -INF
+    logits[36:39, :65536] = 0.0
+    logits[36:39, :65536:2] = -0.0
+    u = torch.tensor(uniform(M, V), device=DEV)
+    t = torch.ones(M, device=DEV)
+    k = torch.tensor(np.resize(np.int32([0, 100, 65535, 65536, 65600, V - 1]), M), device=DEV)
+    p = torch.tensor(np.resize(np.float32([0.5, 0.9, 0.999, 0.1]), M), device=DEV)
+    both(mxg, logits, u, t, k)
+    both(mxg, logits, u, t, None, p)
+    both(mxg, logits, u, t, k, p, torch.tensor(np.resize(np.float32([0, 0.05, 0.5]), M), device=DEV))
+    check(mxg, logits[::3], u[::3].cpu().numpy(), 0.9, 65600, 0.95)
+
+
+def test_sample_batches_at_any_address(mxg):
+    wide = rows(40, 5003, torch.bfloat16, 5)
+    u = torch.tensor(uniform(40, 5), device=DEV)
+    p = torch.full((40,), 0.95, device=DEV)
+    for lo, hi in [(0, 5003), (1, 5002), (3, 3000), (5, 6), (7, 5003), (6, 14)]:
+        both(mxg, wide[:, lo:hi], u, None, None, p)
+    # the mass at one end of long rows: the second pass starts from either
+    logits = rows(40, 150000, torch.bfloat16, 6)
+    logits[:, :20] += torch.linspace(-30, 30, 40, device=DEV)[:, None].bfloat16()
+    logits[:, -20:] += torch.linspace(30, -30, 40, device=DEV)[:, None].bfloat16()
+    logits[::7, 70000:70020] += 25.0
+    for v in (0.0, 0.3, 0.5, 0.7, 0.9999):
+        both(mxg, logits, torch.full_like(u, v), None, None, p)
+
+
+@pytest.mark.parametrize("M", [128, 148, 149, 300])
+def test_sample_batches_beside_the_number_of_sms(mxg, M):
+    logits, u = rows(M, 17001, torch.bfloat16, M), torch.rand(M, device=DEV)
+    p = torch.full((M,), 0.9, device=DEV)
+    both(mxg, logits, u, None, None, p)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = mxg.sample_logits(logits, u, top_p=p)
+        second = mxg.sample_logits(logits, u, top_p=p)
+    logits.copy_(rows(M, 17001, torch.bfloat16, M + 1))
+    graph.replay()
+    want = alone(mxg, logits, u, None, None, p)
+    for got in (first, second):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_sample_batches_without_filters(mxg):
+    logits, u = rows(110, 65543, torch.bfloat16, 3), torch.rand(110, device=DEV)
+    both(mxg, logits, u, torch.rand(110, device=DEV) + 0.5)
+
+
 @pytest.mark.parametrize("M", [1, 5, 32])
 def test_step_with_adapters_head_and_sampler(mxg, M):
     """A decode step of requests with their own adapters and sampling
