@@ -1581,15 +1581,17 @@ SamplePlan plan_sample(int device, int M, int V, bool fp32, bool filtered)
     const int size = fp32 ? 4 : 2;
     SamplePlan pl{};
     const int sms = device_info(device).sms;
-    // A row per SM at a time pays off from a fifth of the SMs on (V = 128256,
-    // top-p: 24 rows 30 us against 35 us of clusters, 64 rows 36 against 55, 148
-    // rows 36 against 106; V = 24000: 24 rows 14 against 17; V = 248320: 24 rows
-    // 54 against 54).  More rows than SMs queue, where clusters of short rows
-    // share SMs (V = 2000: 220 rows 23 us against 14; V = 16384: 28 against 32).
-    // Without top-p and top-k there is no cut to find: many long rows only (V =
-    // 128256: 64 rows 36 against 26, 148 rows 36 against 58).
-    pl.table = !fp32 && (filtered ? 5LL * M >= sms && (M <= sms || V >= 16384)
-                                  : 3LL * M >= 2 * sms && V >= 65536);
+    // A row per SM at a time pays off for short rows, which clusters split for
+    // little (V = 5003: one row 11.2 us against 12.5, 24 rows 12 against 14), and
+    // from a fifth of the SMs on for long ones (V = 128256, top-p: 24 rows 30 us
+    // against 35, 64 rows 36 against 55, 148 rows 36 against 106; V = 248320: 24
+    // rows 54 against 54).  More rows than SMs queue, where clusters of short
+    // rows share SMs (V = 2000: 220 rows 23 us against 14; V = 16384: 28 against
+    // 32).  Without top-p and top-k there is no cut to find: many long rows only
+    // (V = 128256: 64 rows 36 against 26, 148 rows 36 against 58).
+    pl.table = !fp32 && (!filtered ? 3LL * M >= 2 * sms && V >= 65536
+                         : M > sms ? V >= 16384
+                                   : V <= 16384 || 5LL * M >= sms);
     if (pl.table)
         return pl;
     // a CTA per 4096 entries at least while that leaves SMs idle.  Sixteen CTAs
