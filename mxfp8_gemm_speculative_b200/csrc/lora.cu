@@ -27,7 +27,7 @@
 //
 // Measured (B200, graph of calls over rotating buffers): 8192 tokens,
 // 5120 -> 17408, R = 16: 117 us for 658 MB (5.6 TB/s; shrink 24, expand 94);
-// 37 tokens of 48 adapters, 17408 -> 5120, R = 64: 28 us for 72 MB; one token,
+// 37 tokens of 48 adapters, 17408 -> 5120, R = 64: 24 us for 72 MB; one token,
 // 5120 -> 5120: 6.7 us (two kernels of a few dependent steps each).
 #include <algorithm>
 #include <atomic>

@@ -7,9 +7,12 @@
 // so a few rows are bound by latency (the hops between the CTAs of a row) and
 // many rows by the arithmetic per entry.
 //
-// A row is taken by one thread-block cluster: every CTA copies its share into
-// shared memory and everything after that runs on chip, the CTAs exchanging
-// histograms and sums through distributed shared memory.
+// Here a row is taken by one thread-block cluster: every CTA copies its share
+// into shared memory and everything after that runs on chip, the CTAs
+// exchanging histograms and sums through distributed shared memory.  (Batches
+// of bf16 rows and short rows have a kernel of their own further down.)
+// Measured (B200, graph of calls): one row of 248320 bf16 22 us, five of 248320
+// fp32 30 us, 33 of 32003 fp32 without filters 9.7 us.
 //
 //  * Sums are integers.  A weight is an fp64 value in (0, 1], rounded to a
 //    multiple of 2^-44; sums of up to 2^19 of those fit 64 bits and do not
@@ -871,8 +874,13 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
 // entry, against a weight of some 40 instructions and two atomics), computes
 // the weight of every value that occurs once, and finds the cut from the
 // products.  A second pass over the row, out of L2, adds the kept weights per
-// step of 256 entries.  The integers are those of the kernel above, and so are
-// the tokens.
+// step of 256 entries, from the end nearer to the token and no further.  The
+// integers are those of the kernel above, and so are the tokens.
+//
+// Measured: 128 rows of 248320, mixed filters, 58 us (clusters: 161 us), of
+// which the counting pass takes 21 us (14 us of atomics with their bank
+// conflicts), the sums over the counters and the borders 6 us, the second pass
+// 2 to 11 us by the row; 8 rows of 5003 12 us.
 //
 // Counters: word i counts the values of magnitude i, the negative ones in its
 // low half and the positive ones in its high half.  A half that overflows (a
