@@ -198,6 +198,18 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// Four rows r0 .. r3 of a tensor map whose box is one row high, one behind the
+// other in shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, int c0, int r0, int r1,
+                                            int r2, int r3, uint64_t *bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 // Warm L2 with one 2-D tensor-map box (a hint, like prefetch_l2).
 __device__ __forceinline__ void prefetch_tensor_l2(const CUtensorMap *map, int c0, int c1)
 {

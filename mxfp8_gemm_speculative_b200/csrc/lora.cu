@@ -164,9 +164,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // CTAs split K and are added through distributed shared memory in rank order
 // (bitwise reproducible; no atomics, no partial sums in memory).  A producer
 // warp streams a CTA's K range of a group's rows of X and of the adapter's
-// rows of A through a ring in shared memory: A (and X, for a run of more than
-// 16 tokens) as tensor-map boxes of 64 k, other rows of X by asynchronous
-// copies of 16 bytes.  Eight consumer warps run MMAs with the ranks as their
+// rows of A through a ring in shared memory: A as tensor-map boxes of 64 k, X
+// for more than 16 tokens as boxes of 16 rows of a run or as gathers of four
+// rows, for fewer by asynchronous copies of 16 bytes (which for 64 scattered
+// rows took the producer three times the stage's load: 47 us against 36 for 791
+// tokens, 16608 to 3360, R = 32).  Eight consumer warps run MMAs with the ranks as their
 // 16 rows and 8 tokens as their columns; a warp takes every other 16 bytes of
 // a row, and the two halves are added at the end.
 //
@@ -175,12 +177,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // in the batch changes the order of its sums.
 template <int RT>
 struct Shrink {
-    static constexpr int kTok = RT == 4 ? 32 : 64;          // tokens of a group at a time
+    static constexpr int kTok = kBlockTok;                  // tokens of a group at a time
     static constexpr int sub(int rows) { return (rows + 16 * RT) * 128; }   // 64 k of tokens, ranks
     static constexpr int kSubMany = RT == 1 ? 2 : 1, kSubFew = RT == 1 ? 4 : 2;   // per stage
     static constexpr int kMany = kSubMany * sub(kTok), kFewStage = kSubFew * sub(kFew);
     static constexpr int kSlot = kMany > kFewStage ? kMany : kFewStage;
-    static constexpr int kSlots = RT == 1 ? 3 : (RT == 2 ? 7 : 4);
+    static constexpr int kSlots = RT == 1 ? 3 : (RT == 2 ? 7 : 3);
     static constexpr int ST = 16 * RT + 4;                  // row stride of a reduced tile
     static constexpr int kTile = kTok * ST * (int)sizeof(float);
     // ring (aligned to 1024 bytes), tiles of the two halves
@@ -261,6 +263,7 @@ __device__ __forceinline__ void shrink_item(int ntok, int k0, int k1, uint32_t r
 template <int RT>
 __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap x_map,
+                       const __grid_constant__ CUtensorMap x_rows,
                        const __grid_constant__ CUtensorMap a_map, const LoraParams p, int slices,
                        int slice_ranks)
 {
@@ -362,21 +365,30 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
             constexpr bool kIsFew = decltype(few_)::value;
             constexpr int kRows = kIsFew ? kFew : C::kTok;
             constexpr int kSub = kIsFew ? C::kSubFew : C::kSubMany;
-            constexpr int kCopies = kRows / 4;   // rows lane / 8 + 4 i, 16 bytes lane % 8
+            constexpr int kFours = kRows / 4;
             const int n = min(C::kTok, ntok - begin);
             const int m = m0 + list[begin];
             // boxes of 16 tokens, for a run (a few rows are as well copied one by one)
             const bool run = !kIsFew && m0 + list[begin + n - 1] - m == n - 1;
             const int xb = run ? (n + 15) / 16 : 0;
-            const int copies = run ? 0 : (n + 3) / 4;
+            const int fours = run ? 0 : (n + 3) / 4;
+            // few: rows lane / 8 + 4 i, their 16 bytes lane % 8; else gathers
+            // of rows 4 j .. 4 j + 3, j = lane % kFours
             const int c = lane & 7;
-            const uint16_t *src[kCopies];
-            uint32_t dst[kCopies];
+            const uint16_t *src[kIsFew ? kFours : 1];
+            uint32_t dst[kIsFew ? kFours : 1];
+            int row[4] = {};
+            if constexpr (kIsFew) {
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int r = (lane >> 3) + 4 * i;
-                src[i] = p.X + (m0 + list[begin + (r < n ? r : 0)]) * p.ldx + 8 * c;
-                dst[i] = r * 128 + ((c ^ (r & 7)) << 4);
+                for (int i = 0; i < kFours; ++i) {
+                    const int r = (lane >> 3) + 4 * i;
+                    src[i] = p.X + (m0 + list[begin + (r < n ? r : 0)]) * p.ldx + 8 * c;
+                    dst[i] = r * 128 + ((c ^ (r & 7)) << 4);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    row[i] = m0 + list[begin + min(4 * (lane % kFours) + i, n - 1)];
             }
             const int arow = a * p.R + r0;
             // boxes of this item may land where copies of rows did
@@ -392,18 +404,26 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
                 const int nsub = kSub == 1 ? 1 : min(kSub, (k1 - k + 63) / 64);
                 uint8_t *st = dyn + slot * C::kSlot;
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&full[slot], nsub * (slice_ranks + 16 * xb) * 128);
+                    mbar_arrive_expect_tx(&full[slot], nsub * 128 *
+                                                           (slice_ranks + 16 * xb +
+                                                            (kIsFew ? 0 : 4 * fours)));
                 __syncwarp();
                 if (lane < nsub)
                     tma_load_2d(st + lane * C::sub(kRows) + kRows * 128, &a_map, k + 64 * lane, arow,
                                 &full[slot], pol_a);
+                if (!kIsFew && !run && lane < kSub * kFours) {
+                    const int u = lane / kFours, j = lane % kFours;
+                    if (u < nsub && j < fours)
+                        tma_gather4(st + u * C::sub(kRows) + j * 512, &x_rows, k + 64 * u, row[0],
+                                    row[1], row[2], row[3], &full[slot], pol_x);
+                }
                 if (!kIsFew && lane < kSub * (kRows / 16)) {
                     const int u = lane / (kRows / 16), j = lane % (kRows / 16);
                     if (u < nsub && j < xb)
                         tma_load_2d(st + u * C::sub(kRows) + j * 2048, &x_map, k + 64 * u,
                                     m + 16 * j, &full[slot], pol_x);
                 }
-                if (copies > 0) {
+                if constexpr (kIsFew) {
 #pragma unroll
                     for (int u = 0; u < kSub; ++u) {
                         if (u >= nsub)
@@ -411,8 +431,8 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
                         const int kc = k + 64 * u;
                         const bool in = kc + 8 * c < p.K;
 #pragma unroll
-                        for (int i = 0; i < kCopies; ++i) {
-                            if (i >= copies)
+                        for (int i = 0; i < kFours; ++i) {
+                            if (i >= fours)
                                 break;
                             if ((lane >> 3) + 4 * i < n)
                                 cp_async16(smem_u32(st) + u * C::sub(kRows) + dst[i],
@@ -581,7 +601,8 @@ __device__ __forceinline__ int list_parts(const Groups &g, PartTable &tab, bool 
 
 template <int S>
 __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 : 1))
-    lora_expand_kernel(const __grid_constant__ CUtensorMap y_map, const LoraParams p, int blocks,
+    lora_expand_kernel(const __grid_constant__ CUtensorMap y_map,
+                       const __grid_constant__ CUtensorMap y_rows, const LoraParams p, int blocks,
                        int subs)
 {
     using C = Expand<S>;
@@ -689,6 +710,8 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                     run = m0 + table.rows[i][n - 1] - first == n - 1;
                 }
                 const bool box = run && n == 16;
+                // other rows by fours (a batch of fewer than 16 has no maps)
+                const bool gather = !box && n >= 4 && p.M >= 16;
                 const bool new_b = a >= 0 && a != a_last;
                 wait(&empty[slot], phase, 501);
                 if (new_b)
@@ -704,12 +727,20 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                     q.box = box;
                 }
                 __syncwarp();
-                // a box is written whole: zeros stand for its columns past the end
+                // boxes are written whole: zeros stand for columns past the end
                 if (lane == 0)
                     mbar_arrive_expect_tx(&full[slot],
-                                          n * ((box ? C::kCols : cols) * 2 +
-                                               (a < 0 ? 0 : quads * 16)) +
+                                          (box ? 16 * C::kYRow
+                                           : gather ? (n + 3) / 4 * 4 * C::kYRow
+                                                    : n * cols * 2) +
+                                              (a < 0 ? 0 : n * quads * 16) +
                                               (new_b ? cols * p.R * 2 : 0));
+                int row[4];
+                if (gather) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        row[j] = __shfl_sync(0xffffffffu, mine, min(4 * (lane & 3) + j, n - 1));
+                }
                 __syncwarp();
                 // index, B and Y precede the shrink kernel's own wait: they are
                 // read ahead of this kernel's
@@ -728,6 +759,10 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                     if (lane == 0)
                         tma_load_2d(dyn + slot * C::kStage, &y_map, n0, first, &full[slot],
                                     pol_once);
+                } else if (gather) {
+                    if (4 * lane < n)
+                        tma_gather4(dyn + slot * C::kStage + lane * 4 * C::kYRow, &y_rows, n0,
+                                    row[0], row[1], row[2], row[3], &full[slot], pol_once);
                 } else if (lane < n) {
                     bulk_g2s(dyn + slot * C::kStage + lane * C::kYRow, p.Y + mine * p.ldy + n0,
                              cols * 2, &full[slot], pol_once);
@@ -896,20 +931,23 @@ cudaError_t launch_shrink(const LoraPlan &pl, const LoraParams &p, cudaStream_t 
     const cudaError_t e = allow_smem(fn, done, C::smem);
     if (e != cudaSuccess)
         return e;
-    // boxes of 64 k: a slice's ranks of A, 16 tokens of X (which only groups
-    // of more than 16 tokens use)
-    alignas(64) CUtensorMap xm{}, am{};
+    // boxes of 64 k: a slice's ranks of A, 16 tokens or one of X (which only
+    // groups of more than 16 tokens use)
+    alignas(64) CUtensorMap xm{}, xr{}, am{};
     if (!encode_tensor_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.A, (uint64_t)p.K,
                               (uint64_t)p.L * p.R, (uint64_t)p.K * 2, 64,
                               (uint32_t)pl.slice_ranks, CU_TENSOR_MAP_SWIZZLE_128B) ||
         (p.M > kFew &&
-         !encode_tensor_map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.X, (uint64_t)p.K,
-                               (uint64_t)p.M, (uint64_t)p.ldx * 2, 64, 16,
-                               CU_TENSOR_MAP_SWIZZLE_128B)))
+         (!encode_tensor_map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.X, (uint64_t)p.K,
+                                (uint64_t)p.M, (uint64_t)p.ldx * 2, 64, 16,
+                                CU_TENSOR_MAP_SWIZZLE_128B) ||
+          !encode_tensor_map_2d(&xr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.X, (uint64_t)p.K,
+                                (uint64_t)p.M, (uint64_t)p.ldx * 2, 64, 1,
+                                CU_TENSOR_MAP_SWIZZLE_128B))))
         return cudaErrorInvalidValue;
     LoraParams q = p;
     int slices = pl.slices, ranks = pl.slice_ranks;
-    void *args[] = {&xm, &am, &q, &slices, &ranks};
+    void *args[] = {&xm, &xr, &am, &q, &slices, &ranks};
     return launch_pdl_cluster(fn, dim3(pl.cluster, pl.shrink_subs, pl.blocks * pl.slices),
                               dim3(C::kThreads), pl.cluster, C::smem, stream, args);
 }
@@ -922,16 +960,19 @@ cudaError_t launch_expand(const LoraPlan &pl, const LoraParams &p, cudaStream_t 
     const cudaError_t e = allow_smem(fn, done, Expand<S>::smem);
     if (e != cudaSuccess)
         return e;
-    // boxes of 16 tokens x 256 columns (a batch of fewer tokens has none)
-    alignas(64) CUtensorMap ym{};
+    // boxes of 16 tokens or one x 256 columns (a batch of fewer tokens has none)
+    alignas(64) CUtensorMap ym{}, yr{};
     if (p.M >= 16 &&
-        !encode_tensor_map_2d(&ym, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y, (uint64_t)p.N,
-                              (uint64_t)p.M, (uint64_t)p.ldy * 2, Expand<S>::kCols, 16,
-                              CU_TENSOR_MAP_SWIZZLE_NONE))
+        (!encode_tensor_map_2d(&ym, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y, (uint64_t)p.N,
+                               (uint64_t)p.M, (uint64_t)p.ldy * 2, Expand<S>::kCols, 16,
+                               CU_TENSOR_MAP_SWIZZLE_NONE) ||
+         !encode_tensor_map_2d(&yr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y, (uint64_t)p.N,
+                               (uint64_t)p.M, (uint64_t)p.ldy * 2, Expand<S>::kCols, 1,
+                               CU_TENSOR_MAP_SWIZZLE_NONE)))
         return cudaErrorInvalidValue;
     LoraParams q = p;
     int blocks = pl.blocks, subs = pl.expand_subs;
-    void *args[] = {&ym, &q, &blocks, &subs};
+    void *args[] = {&ym, &yr, &q, &blocks, &subs};
     return launch_pdl(fn, dim3(pl.ntiles, pl.expand_shares), dim3(Expand<S>::kThreads),
                       Expand<S>::smem, stream, args);
 }
