@@ -130,6 +130,7 @@ def _ptr(t: torch.Tensor | None):
 # The handle of a device's current stream without a Stream object around it
 # (2 us less per call), where this torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)   # the current device's index
 
 
 def _stream(stream=None, device=None):
@@ -161,8 +162,12 @@ def _on_device(device):
 def _dev_call(device, what: str, fn, *args, stream=None) -> None:
     """fn(*args, stream handle) with ``device`` current; raises on a nonzero
     status."""
-    with _on_device(device):
-        status = fn(*args, _stream(stream, device))
+    if (stream is None and _raw_device is not None and _raw_stream is not None
+            and device.type == "cuda" and device.index == _raw_device()):
+        status = fn(*args, _raw_stream(device.index))   # the same, 1 us less
+    else:
+        with _on_device(device):
+            status = fn(*args, _stream(stream, device))
     if status != MXG_OK:
         raise MxgError(status, what)
 
@@ -718,7 +723,8 @@ _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 def _dense(t: torch.Tensor, dtype, shape, device, name: str) -> int:
     """The pointer of a contiguous tensor of this type and shape."""
-    if not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device.index
+            and t.is_contiguous()):
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         _need_shape(t, shape, name)
@@ -742,7 +748,7 @@ def _empty_as(t: torch.Tensor, dtype, stream) -> torch.Tensor:
 
 def _need_rows(t: torch.Tensor, M: int, N: int, device, name: str) -> int:
     """The row stride of a bf16 [M][N] whose rows are contiguous."""
-    if not (t.dtype is _BF16 and t.shape == (M, N) and t.device == device):
+    if not (t.dtype is _BF16 and t.shape == (M, N) and t.get_device() == device.index):
         if t.dtype != _BF16:
             raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
         if t.shape != (M, N):
@@ -793,7 +799,7 @@ def _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream):
         raise MxgError(MXG_ERR_UNSUPPORTED_SHAPE, "lora_add")
     if out is None:
         if ldy == N and y.is_contiguous():
-            out = _empty_as(y, _BF16, stream)
+            out = torch.empty_like(y) if stream is None else _empty_as(y, _BF16, stream)
         else:
             out = _empty((M, N), _BF16, dev, stream)
         ldo = N
