@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
     auto wait_full = [&](int s, uint32_t parity) { wait_on(&full[s], parity, 541); };
     while (next_item()) {
         const int n = min(C::kTok, ntok - begin);
+        const float sc = p.scales ? __ldg(p.scales + a) : 1.f;   // ahead of its use
         if (n <= kFew)
             shrink_item<RT, kFew, C::kSubFew>(n, k0, k1, smem_u32(dyn), tile, empty, slot, phase,
                                               wait_full, ok);
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
         // ---- add the halves of the CTAs of the cluster in rank order: every
         // CTA finishes a share of the (token, four ranks) entries
         const int quads = ranks / 4;
-        const float sc = p.scales ? __ldg(p.scales + a) : 1.f;
+        uint4 out{}, *to = nullptr;   // stored behind the arrival, which would wait for it
         for (int e = tid * csize + crank; e < n * quads; e += kShrinkWarps * 32 * csize) {
             const int c = e / quads, q = e % quads;
             const float *mine = tile + c * ST + 4 * q;
@@ -501,11 +502,16 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
             split_bf16(s.y * sc, hi[1], lo[1]);
             split_bf16(s.z * sc, hi[2], lo[2]);
             split_bf16(s.w * sc, hi[3], lo[3]);
-            p.T[(size_t)(m0 + list[begin + c]) * (p.R / 4) + r0 / 4 + q] =
-                make_uint4(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16), lo[0] | (lo[1] << 16),
-                           lo[2] | (lo[3] << 16));
+            if (to)
+                *to = out;
+            to = p.T + (size_t)(m0 + list[begin + c]) * (p.R / 4) + r0 / 4 + q;
+            out = make_uint4(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16), lo[0] | (lo[1] << 16),
+                             lo[2] | (lo[3] << 16));
         }
-        cluster_barrier();   // the tiles are read before the next item's
+        cluster_arrive();   // the tiles are read before the next item's
+        if (to)
+            *to = out;
+        cluster_wait();
     }
 }
 
