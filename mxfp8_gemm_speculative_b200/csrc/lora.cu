@@ -114,6 +114,38 @@ __device__ __forceinline__ Groups group_tokens(int raw0, int raw1, int ntok, int
     return g;
 }
 
+// The same by a whole CTA, for more than 32 tokens: each of its first eight
+// warps compares every token with eight others (by one warp, 64 shuffles; by
+// all nine warps of two CTAs of an SM for themselves, a microsecond of them).
+__device__ __forceinline__ Groups group_tokens_cta(int raw0, int raw1, int ntok, int L, int lane,
+                                                   int warp, u64 (&masks)[kBlockTok])
+{
+    Groups g;
+    g.a0 = lane >= ntok ? -2 : raw0 >= 0 && raw0 < L ? raw0 : -1;
+    g.a1 = lane + 32 >= ntok ? -2 : raw1 >= 0 && raw1 < L ? raw1 : -1;
+    if (warp < 8) {
+        uint32_t e0 = 0, e1 = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int l = (8 * warp + i) & 31;
+            const int a = __shfl_sync(0xffffffffu, warp < 4 ? g.a0 : g.a1, l);
+            e0 |= (uint32_t)(a == g.a0) << i;
+            e1 |= (uint32_t)(a == g.a1) << i;
+        }
+        reinterpret_cast<uint8_t *>(&masks[lane])[warp] = (uint8_t)e0;
+        reinterpret_cast<uint8_t *>(&masks[lane + 32])[warp] = (uint8_t)e1;
+    }
+    __syncthreads();
+    g.of0 = masks[lane];
+    g.of1 = masks[lane + 32];
+    const unsigned lead0 =
+        __ballot_sync(0xffffffffu, g.a0 != -2 && __ffsll(g.of0) - 1 == lane);
+    const unsigned lead1 =
+        __ballot_sync(0xffffffffu, g.a1 != -2 && __ffsll(g.of1) - 1 == lane + 32);
+    g.leaders = lead0 | (u64)lead1 << 32;
+    return g;
+}
+
 // The group that token `first` leads: its adapter, its number of tokens, and
 // those (offsets in the block, rising) in this warp's list.
 __device__ __forceinline__ int take_group(const Groups &g, int first, uint8_t *list, int lane,
@@ -270,6 +302,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
     using C = Shrink<RT>;
     constexpr int ST = C::ST;
     __shared__ uint8_t lists[kShrinkWarps + 1][kBlockTok];
+    __shared__ u64 masks[kBlockTok];
     __shared__ uint64_t full[C::kSlots], empty[C::kSlots];
     extern __shared__ uint8_t dyn_raw[];
     // 1024-byte alignment for the swizzled boxes
@@ -297,9 +330,10 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
     const int m0 = block * kBlockTok, r0 = slice * slice_ranks;
     const int ranks = min(slice_ranks, p.R - r0);
     const int btok = min(kBlockTok, p.M - m0);
-    const Groups grp = group_tokens(lane < btok ? __ldcg(p.index + m0 + lane) : -1,
-                                    lane + 32 < btok ? __ldcg(p.index + m0 + lane + 32) : -1, btok,
-                                    p.L, lane);
+    const int raw0 = lane < btok ? __ldcg(p.index + m0 + lane) : -1;
+    const int raw1 = lane + 32 < btok ? __ldcg(p.index + m0 + lane + 32) : -1;
+    const Groups grp = btok > 32 ? group_tokens_cta(raw0, raw1, btok, p.L, lane, warp, masks)
+                                 : group_tokens(raw0, raw1, btok, p.L, lane);
     uint8_t *list = lists[warp];
     const int crank = (int)cluster_rank(), csize = (int)cluster_size();
     const int units = (p.K + 63) / 64;
@@ -616,6 +650,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
     __shared__ uint64_t full[C::kStages], empty[C::kStages];
     __shared__ uint64_t b_empty[C::kBStages];
     __shared__ PartTable table;
+    __shared__ u64 masks[kBlockTok];
     extern __shared__ __align__(128) uint8_t dyn[];
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int n0 = blockIdx.x * C::kCols;
@@ -630,7 +665,31 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             mbar_init(&b_empty[i], C::kConsumers);
         fence_barrier_init();
     }
-    __syncthreads();
+    // the first block's index, grouped by all warps where that is work
+    int block, block_end, sub = 0;
+    if (subs > 1) {
+        block = blockIdx.y % blocks;
+        block_end = block + 1;
+        sub = blockIdx.y / blocks;
+    } else {
+        block = (int)((long long)blockIdx.y * blocks / gridDim.y);
+        block_end = (int)((long long)(blockIdx.y + 1) * blocks / gridDim.y);
+    }
+    int raw0, raw1;
+    auto peek = [&](int b) {
+        const int m = b * kBlockTok + lane;
+        const int end = b < block_end ? min(p.M, (b + 1) * kBlockTok) : 0;
+        raw0 = m < end ? __ldcg(p.index + m) : -1;
+        raw1 = m + 32 < end ? __ldcg(p.index + m + 32) : -1;
+    };
+    peek(block);
+    Groups grp{};
+    bool grouped = p.M - block * kBlockTok > 32;
+    if (grouped)
+        grp = group_tokens_cta(raw0, raw1, min(kBlockTok, p.M - block * kBlockTok), p.L, lane, warp,
+                               masks);
+    else
+        __syncthreads();
     pdl_launch_dependents();
     // by whole warps; once a wait has run out the role goes to its end
     bool ok = true;
@@ -644,24 +703,6 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
 
     if (warp == C::kConsumers) {
         // ------------------------------------------------------- producer
-        int block, block_end, sub = 0;
-        if (subs > 1) {
-            block = blockIdx.y % blocks;
-            block_end = block + 1;
-            sub = blockIdx.y / blocks;
-        } else {
-            block = (int)((long long)blockIdx.y * blocks / gridDim.y);
-            block_end = (int)((long long)(blockIdx.y + 1) * blocks / gridDim.y);
-        }
-        // the index of the next block, ahead of its use
-        int raw0, raw1;
-        auto peek = [&](int b) {
-            const int m = b * kBlockTok + lane;
-            const int end = b < block_end ? min(p.M, (b + 1) * kBlockTok) : 0;
-            raw0 = m < end ? __ldcg(p.index + m) : -1;
-            raw1 = m + 32 < end ? __ldcg(p.index + m + 32) : -1;
-        };
-        peek(block);
         const bool in_place = p.Out == p.Y;
         const uint64_t pol_once = l2_policy_evict_first(), pol_keep = l2_policy_evict_last();
         int slot = 0, b_slot = 0;
@@ -698,11 +739,13 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             if (one) {
                 nparts = (a0 < 0 || a0 >= p.L) && in_place ? 0 : kBlockTok / 16;
             } else {
-                const Groups grp = group_tokens(raw0, raw1, min(kBlockTok, p.M - m0), p.L, lane);
+                if (!grouped)
+                    grp = group_tokens(raw0, raw1, min(kBlockTok, p.M - m0), p.L, lane);
                 __syncwarp();
                 nparts = list_parts(grp, table, in_place, lane);
             }
-            peek(block + 1);
+            grouped = false;
+            peek(block + 1);   // ahead of its use
             for (int i = sub; i < nparts; i += subs) {
                 if (!waited && before == C::kAhead)
                     wait_shrink();
