@@ -668,12 +668,13 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
     // the first block's index, grouped by all warps where that is work
     int block, block_end, sub = 0;
     if (subs > 1) {
-        block = blockIdx.y % blocks;
+        block = blocks == 1 ? 0 : blockIdx.y % blocks;
         block_end = block + 1;
-        sub = blockIdx.y / blocks;
+        sub = blocks == 1 ? blockIdx.y : blockIdx.y / blocks;
     } else {
-        block = (int)((long long)blockIdx.y * blocks / gridDim.y);
-        block_end = (int)((long long)(blockIdx.y + 1) * blocks / gridDim.y);
+        // (blocks < 2^15 and a few hundred CTAs: 32 bits)
+        block = (int)(blockIdx.y * (unsigned)blocks / gridDim.y);
+        block_end = (int)((blockIdx.y + 1) * (unsigned)blocks / gridDim.y);
     }
     int raw0, raw1;
     auto peek = [&](int b) {
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             for (int s = 0; s < before; ++s)
                 copy_t(s);
         };
-        bool wrapped = false;
+        bool wrapped = false, b_wrapped = false;
         int a_last = -1;
         for (; block < block_end && ok; ++block) {
             const int m0 = block * kBlockTok;
@@ -762,8 +763,10 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                 // other rows by fours (a batch of fewer than 16 has no maps)
                 const bool gather = !box && n >= 4 && p.M >= 16;
                 const bool new_b = a >= 0 && a != a_last;
-                wait(&empty[slot], phase, 501);
-                if (new_b)
+                // (a test of a barrier takes 150 cycles: none in the first round)
+                if (wrapped)
+                    wait(&empty[slot], phase, 501);
+                if (new_b && b_wrapped)
                     wait(&b_empty[b_slot], b_phase, 502);
                 if (!ok)
                     break;
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                 if (gather) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        row[j] = __shfl_sync(0xffffffffu, mine, min(4 * (lane & 3) + j, n - 1));
+                        row[j] = m0 + table.rows[i][min(4 * (lane & 3) + j, n - 1)];
                 }
                 __syncwarp();
                 // index, B and Y precede the shrink kernel's own wait: they are
@@ -802,6 +805,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                     if (++b_slot == C::kBStages) {
                         b_slot = 0;
                         b_phase ^= 1;
+                        b_wrapped = true;
                     }
                 }
                 if (box) {
@@ -829,7 +833,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
         }
         if (!waited)
             wait_shrink();
-        if (ok)
+        if (ok && wrapped)
             wait(&empty[slot], phase, 503);
         if (ok) {
             // the end of the list
