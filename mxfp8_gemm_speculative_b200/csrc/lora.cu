@@ -26,9 +26,9 @@
 // block that uses it and once in all for up to 64 tokens.
 //
 // Measured (B200, graph of calls over rotating buffers): 8192 tokens,
-// 5120 -> 17408, R = 16: 117 us for 658 MB (5.6 TB/s; shrink 24, expand 94);
-// 37 tokens of 48 adapters, 17408 -> 5120, R = 64: 24 us for 72 MB; one token,
-// 5120 -> 5120: 6.7 us (two kernels of a few dependent steps each).
+// 5120 -> 17408, R = 16: 118 us for 658 MB (5.6 TB/s; shrink 24, expand 94);
+// 37 tokens of 48 adapters, 17408 -> 5120, R = 64: 23 us for 72 MB; one token,
+// 5120 -> 5120: 6.8 us (two kernels of a few dependent steps each).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
