@@ -291,3 +291,28 @@ def test_lora_calls_at_once_on_two_streams(mxg):
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("share", [1, 3, 4, 5, 15, 16, 17, 33, 64])
+@pytest.mark.parametrize("R", [8, 32, 64, 128])
+def test_lora_scattered_groups_of_every_size(mxg, share, R):
+    """`share` tokens of every 64 have the first adapter, the others the second
+    or none, in any order: rows in fours, with some left over, of column ranges
+    whose neighbours hold NaN."""
+    M, K, N = 147, 200, 312
+    g = torch.Generator(device=DEV)
+    g.manual_seed(share)
+    index = torch.cat([torch.where(torch.randperm(64, generator=g, device=DEV) < share, 0, i % 2 * 2 - 1)
+                       for i in range(3)])[:M]
+    x, a, b, index, y, s = case(M, K, N, R, 2, seed=R, index=index)
+    wide_x = torch.full((M, K + 24), float("nan"), device=DEV).bfloat16()
+    wide_y = torch.full((M, N + 40), float("nan"), device=DEV).bfloat16()
+    wide_x[:, 16:16 + K] = x
+    wide_y[:, 8:8 + N] = y
+    got = mxg.lora_add(wide_x[:, 16:16 + K], a, b, index, wide_y[:, 8:8 + N], scales=s)
+    check(got, x, a, b, index, y, s)
+    # by themselves, in a run of rows: the same bits
+    mine = (index == 0).nonzero()[:, 0]
+    alone = mxg.lora_add(x[mine].contiguous(), a, b, index[mine].contiguous(),
+                         y[mine].contiguous(), scales=s)
+    assert torch.equal(alone, got[mine])
