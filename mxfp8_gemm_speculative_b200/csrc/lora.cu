@@ -26,7 +26,7 @@
 // block that uses it and once in all for up to 64 tokens.
 //
 // Measured (B200, graph of calls over rotating buffers): 8192 tokens,
-// 5120 -> 17408, R = 16: 118 us for 658 MB (5.6 TB/s; shrink 24, expand 94);
+// 5120 -> 17408, R = 16: 116 us for 658 MB (5.7 TB/s; shrink 23, expand 93);
 // 37 tokens of 48 adapters, 17408 -> 5120, R = 64: 23 us for 72 MB; one token,
 // 5120 -> 5120: 6.8 us (two kernels of a few dependent steps each).
 #include <algorithm>
@@ -559,7 +559,8 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
 // eight consumer warps work on 32 columns each.  Sixteen consecutive tokens
 // are one tensor-map box; others are copied row by row (a copy costs the
 // engine some 35 cycles whatever its size: row copies alone made a prefill
-// chunk 1.6 times slower than plain loads).
+// chunk 1.6 times slower than plain loads; gathers of four rows, even where no
+// part took them, cost a prefill chunk 3 us of 117 and gave scattered tokens 3 %).
 //
 // MMAs have the part's tokens as their 16 rows and 8 columns each; column c of
 // MMA i is column 8 (c / 2) + 2 i + c % 2 of the warp's 32, so a lane's
@@ -641,8 +642,7 @@ __device__ __forceinline__ int list_parts(const Groups &g, PartTable &tab, bool 
 
 template <int S>
 __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 : 1))
-    lora_expand_kernel(const __grid_constant__ CUtensorMap y_map,
-                       const __grid_constant__ CUtensorMap y_rows, const LoraParams p, int blocks,
+    lora_expand_kernel(const __grid_constant__ CUtensorMap y_map, const LoraParams p, int blocks,
                        int subs)
 {
     using C = Expand<S>;
@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             mbar_init(&b_empty[i], C::kConsumers);
         fence_barrier_init();
     }
-    // the first block's index, grouped by all warps where that is work
+    // the first block's index, grouped by all warps where that is work and
+    // the CTA has no other block
     int block, block_end, sub = 0;
     if (subs > 1) {
         block = blocks == 1 ? 0 : blockIdx.y % blocks;
@@ -683,14 +684,15 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
         raw0 = m < end ? __ldcg(p.index + m) : -1;
         raw1 = m + 32 < end ? __ldcg(p.index + m + 32) : -1;
     };
-    peek(block);
     Groups grp{};
-    bool grouped = p.M - block * kBlockTok > 32;
-    if (grouped)
+    bool grouped = subs > 1 && p.M - block * kBlockTok > 32;
+    if (grouped) {
+        peek(block);
         grp = group_tokens_cta(raw0, raw1, min(kBlockTok, p.M - block * kBlockTok), p.L, lane, warp,
                                masks);
-    else
+    } else {
         __syncthreads();
+    }
     pdl_launch_dependents();
     // by whole warps; once a wait has run out the role goes to its end
     bool ok = true;
@@ -704,6 +706,8 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
 
     if (warp == C::kConsumers) {
         // ------------------------------------------------------- producer
+        if (!grouped)
+            peek(block);
         const bool in_place = p.Out == p.Y;
         const uint64_t pol_once = l2_policy_evict_first(), pol_keep = l2_policy_evict_last();
         int slot = 0, b_slot = 0;
@@ -760,8 +764,6 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                     run = m0 + table.rows[i][n - 1] - first == n - 1;
                 }
                 const bool box = run && n == 16;
-                // other rows by fours (a batch of fewer than 16 has no maps)
-                const bool gather = !box && n >= 4 && p.M >= 16;
                 const bool new_b = a >= 0 && a != a_last;
                 // (a test of a barrier takes 150 cycles: none in the first round)
                 if (wrapped)
@@ -779,20 +781,12 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                     q.box = box;
                 }
                 __syncwarp();
-                // boxes are written whole: zeros stand for columns past the end
+                // a box is written whole: zeros stand for its columns past the end
                 if (lane == 0)
                     mbar_arrive_expect_tx(&full[slot],
-                                          (box ? 16 * C::kYRow
-                                           : gather ? (n + 3) / 4 * 4 * C::kYRow
-                                                    : n * cols * 2) +
-                                              (a < 0 ? 0 : n * quads * 16) +
+                                          n * ((box ? C::kCols : cols) * 2 +
+                                               (a < 0 ? 0 : quads * 16)) +
                                               (new_b ? cols * p.R * 2 : 0));
-                int row[4];
-                if (gather) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        row[j] = m0 + table.rows[i][min(4 * (lane & 3) + j, n - 1)];
-                }
                 __syncwarp();
                 // index, B and Y precede the shrink kernel's own wait: they are
                 // read ahead of this kernel's
@@ -812,10 +806,6 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                     if (lane == 0)
                         tma_load_2d(dyn + slot * C::kStage, &y_map, n0, first, &full[slot],
                                     pol_once);
-                } else if (gather) {
-                    if (4 * lane < n)
-                        tma_gather4(dyn + slot * C::kStage + lane * 4 * C::kYRow, &y_rows, n0,
-                                    row[0], row[1], row[2], row[3], &full[slot], pol_once);
                 } else if (lane < n) {
                     bulk_g2s(dyn + slot * C::kStage + lane * C::kYRow, p.Y + mine * p.ldy + n0,
                              cols * 2, &full[slot], pol_once);
@@ -1013,19 +1003,16 @@ cudaError_t launch_expand(const LoraPlan &pl, const LoraParams &p, cudaStream_t 
     const cudaError_t e = allow_smem(fn, done, Expand<S>::smem);
     if (e != cudaSuccess)
         return e;
-    // boxes of 16 tokens or one x 256 columns (a batch of fewer tokens has none)
-    alignas(64) CUtensorMap ym{}, yr{};
+    // boxes of 16 tokens x 256 columns (a batch of fewer tokens has none)
+    alignas(64) CUtensorMap ym{};
     if (p.M >= 16 &&
-        (!encode_tensor_map_2d(&ym, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y, (uint64_t)p.N,
-                               (uint64_t)p.M, (uint64_t)p.ldy * 2, Expand<S>::kCols, 16,
-                               CU_TENSOR_MAP_SWIZZLE_NONE) ||
-         !encode_tensor_map_2d(&yr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y, (uint64_t)p.N,
-                               (uint64_t)p.M, (uint64_t)p.ldy * 2, Expand<S>::kCols, 1,
-                               CU_TENSOR_MAP_SWIZZLE_NONE)))
+        !encode_tensor_map_2d(&ym, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y, (uint64_t)p.N,
+                              (uint64_t)p.M, (uint64_t)p.ldy * 2, Expand<S>::kCols, 16,
+                              CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     LoraParams q = p;
     int blocks = pl.blocks, subs = pl.expand_subs;
-    void *args[] = {&ym, &yr, &q, &blocks, &subs};
+    void *args[] = {&ym, &q, &blocks, &subs};
     return launch_pdl(fn, dim3(pl.ntiles, pl.expand_shares), dim3(Expand<S>::kThreads),
                       Expand<S>::smem, stream, args);
 }
