@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
     auto wait_full = [&](int s, uint32_t parity) { wait_on(&full[s], parity, 541); };
     while (next_item()) {
         const int n = min(C::kTok, ntok - begin);
-        const float sc = p.scales ? __ldg(p.scales + a) : 1.f;   // ahead of its use
+        const float sc = p.scales ? __ldcg(p.scales + a) : 1.f;   // ahead of its use
         if (n <= kFew)
             shrink_item<RT, kFew, C::kSubFew>(n, k0, k1, smem_u32(dyn), tile, empty, slot, phase,
                                               wait_full, ok);

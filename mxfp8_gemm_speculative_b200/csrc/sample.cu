@@ -448,11 +448,11 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
         data[i] = bits_of<T>(-INFINITY);
     pdl_wait();
     pdl_launch_dependents();
-    const float temp = p.temperature ? __ldg(p.temperature + row) : 1.f;
-    const float top_p = p.top_p ? __ldg(p.top_p + row) : 1.f;
-    const float min_p = p.min_p ? __ldg(p.min_p + row) : 0.f;
-    const int top_k = p.top_k ? __ldg(p.top_k + row) : 0;
-    const float u = __ldg(p.u + row);
+    const float temp = p.temperature ? __ldcg(p.temperature + row) : 1.f;
+    const float top_p = p.top_p ? __ldcg(p.top_p + row) : 1.f;
+    const float min_p = p.min_p ? __ldcg(p.min_p + row) : 0.f;
+    const int top_k = p.top_k ? __ldcg(p.top_k + row) : 0;
+    const float u = __ldcg(p.u + row);
 
     // ---- copy the entries and find the maximum
     float mx = -INFINITY;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(1024, 1) sample_kernel(const SampleParams p)
         }
         if (tid < cnt - vecs * kVec) {   // what the vectors leave: fewer than 2 kVec entries
             const int i = tid < head ? tid : tid + vecs * kVec;
-            const float a = canonical(value_of(src[i]));
+            const float a = canonical(value_of(__ldcg(src + i)));
             data[skew + i] = bits_of<T>(a);
             mx = fmaxf(mx, a);
         }
@@ -983,8 +983,8 @@ __global__ void __launch_bounds__(kTableThreads, 1) sample_table_kernel(const Sa
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int a = e + 2 * j, b = a + 1;
-            w[j] = (a >= 0 && a < p.V ? src[a] : 0xFF80u) |
-                   (b >= 0 && b < p.V ? (uint32_t)src[b] : 0xFF80u) << 16;
+            w[j] = (a >= 0 && a < p.V ? __ldcg(src + a) : 0xFF80u) |
+                   (b >= 0 && b < p.V ? (uint32_t)__ldcg(src + b) : 0xFF80u) << 16;
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     };
@@ -1029,11 +1029,11 @@ __global__ void __launch_bounds__(kTableThreads, 1) sample_table_kernel(const Sa
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    const float temp = p.temperature ? __ldg(p.temperature + row) : 1.f;
-    const float top_p = p.top_p ? __ldg(p.top_p + row) : 1.f;
-    const float min_p = p.min_p ? __ldg(p.min_p + row) : 0.f;
-    const int top_k = p.top_k ? __ldg(p.top_k + row) : 0;
-    const float u = __ldg(p.u + row);
+    const float temp = p.temperature ? __ldcg(p.temperature + row) : 1.f;
+    const float top_p = p.top_p ? __ldcg(p.top_p + row) : 1.f;
+    const float min_p = p.min_p ? __ldcg(p.min_p + row) : 0.f;
+    const int top_k = p.top_k ? __ldcg(p.top_k + row) : 0;
+    const float u = __ldcg(p.u + row);
     const bool greedy = __any_sync(0xffffffffu, !(temp > 0.f));
 
     // ---- first pass: the largest key, and how often each occurs
