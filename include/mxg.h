@@ -445,6 +445,17 @@ MXG_API int mxfp8_dequant(const uint8_t *Wq, const uint8_t *Ws, int N, int K,
  * *status receives MXG_OK or the first error a kernel recorded. */
 MXG_API int mxg_workspace_status(const void *workspace, int *status, cudaStream_t stream);
 
+/* The weight-streaming kernel's ring for a shape on a device of `sms` SMs and
+ * `smem_bytes` of dynamic shared memory a block, worked out on the host
+ * without a device: its stages, and how many warps take a tile's stages in
+ * turn.  Whole turns go round the ring (*stages % *turns == 0): a warp that
+ * meets a slot again has waited for the slot's last filling itself, without
+ * which its wait for the next one could end early.
+ * bits: 4 (INT4), 8 (INT8) or 0 (re-packed MXFP8; group_size is not used).
+ * A shape that kernel does not take: MXG_ERR_UNSUPPORTED_SHAPE. */
+MXG_API int mxg_selftest_stream_ring(int bits, int M, int N, int K, int group_size, int sms,
+                  int smem_bytes, int *stages, int *turns);
+
 /* Runs one CTA whose pipeline wait can never complete (nothing arrives on
  * its barrier) with a time limit of `limit_us` microseconds, to exercise the
  * timeout path.  The kernel records MXG_ERR_TIMEOUT in the workspace status

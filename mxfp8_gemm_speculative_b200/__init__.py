@@ -62,6 +62,7 @@ _SIGS = {
     "mxfp8_dequant": (_i, [_p, _p, _i, _i, _p, _p]),
     "mxg_workspace_status": (_i, [_p, ctypes.POINTER(_i), _p]),
     "mxg_selftest_wait_timeout": (_i, [_p, _i, _p]),
+    "mxg_selftest_stream_ring": (_i, [_i, _i, _i, _i, _i, _i, _i, _p, _p]),
     "w8a16_packed_bytes": (_sz, [_i, _i, _i]),
     "w8a16_repack": (_i, [_p, _p, _i, _i, _i, _p, _p]),
     "w8a16_repack_ct": (_i, [_p, _p, _i, _i, _i, _p, _p]),
@@ -945,6 +946,18 @@ def w8a16_gemm_sample(x: torch.Tensor, packed: torch.Tensor, N: int, K: int, u: 
                stream=stream)
     _dev_call(x.device, "sample_logits", _lib.sample_logits, *args, stream=stream)
     return *outs, logits
+
+
+def mxg_selftest_stream_ring(bits: int, M: int, N: int, K: int, group_size: int = 128,
+                             sms: int = 148, smem_bytes: int = 227 * 1024):
+    """(stages, turns) of the weight-streaming kernel's ring for a shape, from
+    the host's plan alone: ``bits`` 4 (INT4), 8 (INT8) or 0 (re-packed
+    MXFP8)."""
+    stages, turns = ctypes.c_int(0), ctypes.c_int(0)
+    _check(_lib.mxg_selftest_stream_ring(bits, M, N, K, group_size, sms, smem_bytes,
+                                         ctypes.byref(stages), ctypes.byref(turns)),
+           "mxg_selftest_stream_ring")
+    return stages.value, turns.value
 
 
 def mxg_selftest_wait_timeout(workspace_buf: torch.Tensor | None, limit_us: int,

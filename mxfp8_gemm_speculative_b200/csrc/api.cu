@@ -630,6 +630,19 @@ int mxg_workspace_status(const void *workspace, int *status, cudaStream_t stream
     return MXG_OK;
 }
 
+int mxg_selftest_stream_ring(int bits, int M, int N, int K, int group_size, int sms, int smem_bytes,
+                             int *stages, int *turns)
+{
+    if ((bits != 0 && bits != 4 && bits != 8) || sms < 1 || smem_bytes < 1 || !stages || !turns)
+        return MXG_ERR_INVALID_ARG;
+    if (bits != 0 && !w4a16_shape_ok(K, N, group_size))
+        return MXG_ERR_UNSUPPORTED_SHAPE;
+    const DeviceInfo di{sms, smem_bytes};
+    return stream_ring(di, M, N, K, bits == 0 ? 64 : group_size, bits, stages, turns)
+               ? MXG_OK
+               : MXG_ERR_UNSUPPORTED_SHAPE;
+}
+
 int mxg_selftest_wait_timeout(void *workspace, int limit_us, cudaStream_t stream)
 {
     if ((workspace && !aligned16(workspace)) || limit_us < 1 || limit_us > 10000000)

@@ -64,6 +64,10 @@ bool plan_w8a16_stream(int device, int M, int N, int K, int G, StreamPlan *plan)
 // Re-packed MXFP8 (mxfp8_repack) on the same kernel, M <= 16; launch with
 // launch_w4a16_stream and G = 64.
 bool plan_mxfp8_packed_stream(int device, int M, int N, int K, StreamPlan *plan);
+// The ring stages that plan gives a shape on a device of these facts (bits: 4,
+// 8, or 0 for re-packed MXFP8), and the warps that take a tile's stages in turn.
+bool stream_ring(const DeviceInfo &di, int M, int N, int K, int G, int bits, int *stages,
+                 int *turns);
 // early: load the first weights before waiting for the previous kernel on
 // the stream (every launch function below takes it per call).
 cudaError_t launch_w4a16_stream(const StreamPlan &plan, const void *X, const void *packed, int M,

@@ -126,7 +126,7 @@ struct Params {
     int upr;                 // units (stages) per group row: ceil(K / 128)
     int q, r;                // stream-K: units = q * ctas + r: CTAs below r run q + 1 units
     int S;                   // pieces per group row (row split), or 0 (stream-K)
-    int R;                   // ring stages
+    int R;                   // ring stages, a multiple of kWPT
     int x_off, xs_off, xchg_off, bar_off;   // shared-memory regions (bytes from the base)
     int early;               // load the first weights before waiting for the previous kernel
     int pf_stages;           // stages after the ring warmed in L2 at entry
@@ -918,7 +918,7 @@ const void *select_kernel(int tt, int variant)
 }
 
 struct VariantCfg {
-    int stage, xchg, threads, consumers, g, xbox;
+    int stage, xchg, threads, consumers, g, xbox, wpt;
 };
 
 template <int TT, int V>
@@ -926,7 +926,7 @@ VariantCfg cfg_one()
 {
     using W = VariantOf<V>;
     using C = Cfg<TT, W::kGM, W::kP, W::kXR>;
-    return {C::kStage, C::kXchg, C::kThreads, C::kConsumers, C::kG, C::kXBox};
+    return {C::kStage, C::kXchg, C::kThreads, C::kConsumers, C::kG, C::kXBox, C::kWPT};
 }
 
 VariantCfg variant_cfg(int tt, int v)
@@ -968,17 +968,15 @@ SmemPlan smem_plan(const VariantCfg &vc, int R, int xbytes, int xsbytes)
     return s;
 }
 
+// The plan for a device of these facts, without touching it.
 // bits: 4 (INT4), 8 (INT8, two code planes) or 0 (re-packed MXFP8: G = 64
 // chunks, resident activations only, so M <= 16)
-bool plan_stream(int device, int M, int N, int K, int G, int bits, StreamPlan *plan)
+bool plan_geometry(const DeviceInfo &di, int M, int N, int K, int G, int bits, StreamPlan *plan)
 {
-    if (M < 1 || M > 32 || N % 64 != 0 || K % 64 != 0 || K % G != 0)
+    if (M < 1 || M > 32 || N < 64 || K < 64 || N % 64 != 0 || K % 64 != 0 || K % G != 0)
         return false;
     if (bits == 0 && (G != 64 || M > 16))
         return false;
-    if (device < 0 || device >= kMaxDeviceCache)
-        return false;
-    const DeviceInfo &di = device_info(device);
     StreamPlan pl{};
     pl.tt = (M + 7) / 8;
     const int ntiles = N / 32;
@@ -1035,10 +1033,17 @@ bool plan_stream(int device, int M, int N, int K, int G, int bits, StreamPlan *p
     const VariantCfg vc = variant_cfg(pl.tt, pl.variant);
     if (!xr)
         xbytes = xsbytes = 0;
-    // the deepest ring that fits, up to MXG_STREAM_MAX_RING_KB of stages
+    // The deepest ring that fits, up to MXG_STREAM_MAX_RING_KB of stages, in
+    // whole turns of a tile's warps, so that every filling of a slot is taken
+    // by the same warp of a tile.  With an odd ring under two warps a slot's
+    // fillings would go to them by turns; neither would wait for the ones
+    // between its own, and a wait for filling n, while n - 1 is still on its
+    // way, returns at once (the phase it names has the parity of the one
+    // before): the warp would multiply what lay in the slot.
     int R = (MXG_STREAM_MAX_RING_KB * 1024) / vc.stage;
     while (R > 2 && (int)smem_plan(vc, R, xbytes, xsbytes).total > budget)
         --R;
+    R -= R % vc.wpt;
     if (R < 3)
         return false;
     const SmemPlan sp = smem_plan(vc, R, xbytes, xsbytes);
@@ -1049,6 +1054,21 @@ bool plan_stream(int device, int M, int N, int K, int G, int bits, StreamPlan *p
     pl.xchg_off = sp.xchg_off;
     pl.bar_off = sp.bar_off;
     pl.warps_per_cta = vc.threads / 32;
+    pl.partial_bytes = (size_t)pl.Wt * 2 * kWarps * (2 * pl.tt * 32) * sizeof(float4);
+    *plan = pl;
+    return true;
+}
+
+bool plan_stream(int device, int M, int N, int K, int G, int bits, StreamPlan *plan)
+{
+    if (device < 0 || device >= kMaxDeviceCache)
+        return false;
+    const DeviceInfo &di = device_info(device);
+    StreamPlan pl{};
+    if (!plan_geometry(di, M, N, K, G, bits, &pl))
+        return false;
+    const VariantCfg vc = variant_cfg(pl.tt, pl.variant);
+    const int budget = std::min(di.smem_optin, kMaxSmem);
     const void *fn = select_kernel(pl.tt, pl.variant);
     if (!fn)
         return false;
@@ -1067,7 +1087,6 @@ bool plan_stream(int device, int M, int N, int K, int G, int bits, StreamPlan *p
             return false;
         occ_slot.store(o, std::memory_order_release);
     }
-    pl.partial_bytes = (size_t)pl.Wt * 2 * kWarps * (2 * pl.tt * 32) * sizeof(float4);
     *plan = pl;
     return true;
 }
@@ -1087,6 +1106,16 @@ bool plan_w8a16_stream(int device, int M, int N, int K, int G, StreamPlan *plan)
 bool plan_mxfp8_packed_stream(int device, int M, int N, int K, StreamPlan *plan)
 {
     return plan_stream(device, M, N, K, 64, 0, plan);
+}
+
+bool stream_ring(const DeviceInfo &di, int M, int N, int K, int G, int bits, int *stages, int *turns)
+{
+    StreamPlan pl{};
+    if (!plan_geometry(di, M, N, K, G, bits, &pl))
+        return false;
+    *stages = pl.ring;
+    *turns = variant_cfg(pl.tt, pl.variant).wpt;
+    return true;
 }
 
 cudaError_t launch_w4a16_stream(const StreamPlan &pl, const void *X, const void *packed, int M,
