@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
         uint32_t phase = 1;         // of the empty barriers: the first round is free
         bool wrapped = false;
         bool owed = false;          // the last item's barriers
+        uint32_t copied = 0;        // slots that 16-byte copies wrote last
         auto barriers = [&]() {
             cluster_barrier();
             cluster_barrier();
@@ -425,8 +426,6 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
                     row[i] = m0 + list[begin + min(4 * (lane % kFours) + i, n - 1)];
             }
             const int arow = a * p.R + r0;
-            // boxes of this item may land where copies of rows did
-            fence_proxy_async_smem();
             int s = 0;
             for (int k = k0; k < k1; k += 64 * kSub, ++s) {
                 // the ring may run ahead of the last item's end by its own size
@@ -435,6 +434,12 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
                 wait_on(&empty[slot], phase, 531);
                 if (!ok)
                     break;
+                // Boxes of many tokens land where copies of few did: those are
+                // complete now (the consumers that freed the slot waited for
+                // them), and the fence puts them before the boxes.
+                if (!kIsFew && copied >> slot & 1)
+                    fence_proxy_async_smem();
+                copied = kIsFew ? copied | 1u << slot : copied & ~(1u << slot);
                 const int nsub = kSub == 1 ? 1 : min(kSub, (k1 - k + 63) / 64);
                 uint8_t *st = dyn + slot * C::kSlot;
                 if (lane == 0)
