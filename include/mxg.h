@@ -377,10 +377,9 @@ MXG_API int bf16_gemm_small_ex(const void *X, const void *W, int M, int N, int K
  *           X * A^T.  Needs no initialisation and keeps nothing that a later
  *           call reads.  Not the workspace of a call that may run at the same
  *           time, nor one that a GEMM uses (those keep their counters in it).
- * The inner products are held to 16 bits of mantissa at least (not rounded to
- * bf16), sums in fp32; Out is rounded once.  Bitwise reproducible.  Unlike the
- * GEMMs, nothing is read before the previous kernel on `stream` has
- * completed: A, B and index may be what it writes.
+ * The inner products and all sums are held in fp32; Out is rounded once.
+ * Bitwise reproducible.  Unlike the GEMMs, nothing is read before the previous
+ * kernel on `stream` has completed: A, B and index may be what it writes.
  * 1 <= M <= 2097088; K, N, R >= 8 and multiples of 8; R <= 128;
  * L * R < 2^31; strides multiples of 8.  Other sizes: MXG_ERR_UNSUPPORTED_SHAPE; a stride
  * below its row or not a multiple of 8, L < 1: MXG_ERR_INVALID_ARG. */

@@ -14,11 +14,10 @@
 // in a decode batch.
 //
 // Two kernels, joined by programmatic dependent launch:
-//   shrink   T = s * X A^T, [M][R] in fp32, kept as two bf16 halves
-//            (T = hi + lo, 16 bits of mantissa at least: the inner product
-//            is not rounded to bf16 on its way, at the price of twice the
-//            MMAs of the expand kernel);
-//   expand   Out = Y + T B^T, summed in fp32 and rounded once.
+//   shrink   T = s * X A^T, [M][R] in fp32;
+//   expand   Out = Y + T B^T, T as three bf16 of eight bits of mantissa each
+//            (the inner product keeps its 24 bits, at the price of three times
+//            the MMAs), summed in fp32 and rounded once.
 //
 // Tokens come in any order.  Both kernels take blocks of 64 consecutive tokens
 // and group a block's tokens by adapter with warp instructions (no sort
@@ -26,7 +25,7 @@
 // block that uses it and once in all for up to 64 tokens.
 //
 // Measured (B200, graph of calls over rotating buffers): 8192 tokens,
-// 5120 -> 17408, R = 16: 116 us for 658 MB (5.7 TB/s; shrink 23, expand 93);
+// 5120 -> 17408, R = 16: 128 us for 658 MB (5.1 TB/s; shrink 23, expand 105);
 // 37 tokens of 48 adapters, 17408 -> 5120, R = 64: 23 us for 72 MB; one token,
 // 5120 -> 5120: 6.8 us (two kernels of a few dependent steps each).
 #include <algorithm>
@@ -51,7 +50,7 @@ struct LoraParams {
     const float *scales;     // [L] or NULL (all 1)
     const int *index;        // [M]
     WsHeader *hdr;           // status word, cleared by the shrink kernel
-    uint4 *T;                // [M][R / 4]: four hi halves, then four lo halves
+    float4 *T;               // fp32 [M][R]
     long long ldx, ldy, ldo; // row strides in elements
     int M, N, K, R, L;
 };
@@ -174,13 +173,50 @@ __device__ __forceinline__ float4 ld_peer_f4(const void *p, uint32_t rank)
     return v;
 }
 
-// fp32 v = hi + lo in bf16; a value without a finite hi has no lo.
-__device__ __forceinline__ void split_bf16(float v, uint32_t &hi, uint32_t &lo)
+// Four fp32 values as sums of three bf16 each, by truncation: eight bits of
+// mantissa go to `hi`, the next eight to `mid`, the last to `lo` (all 24, but
+// for bits below 2^-133).  Pairs, in the order of the values.
+struct Split {
+    uint32_t hi[2], mid[2], lo[2];
+};
+__device__ __forceinline__ Split split_f32(const uint4 &v)
 {
-    hi = f32_to_bf16_bits(v);
-    const float back = __uint_as_float(hi << 16);
-    const float rest = v - back;
-    lo = (hi & 0x7F80u) == 0x7F80u ? 0u : f32_to_bf16_bits(rest);
+    const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float r = __uint_as_float(b[i]) - __uint_as_float(b[i] & 0xFFFF0000u);
+        m[i] = __float_as_uint(r);
+        l[i] = __float_as_uint(r - __uint_as_float(m[i] & 0xFFFF0000u));
+    }
+    Split s;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        s.hi[i] = __byte_perm(b[2 * i], b[2 * i + 1], 0x7632);
+        s.mid[i] = __byte_perm(m[2 * i], m[2 * i + 1], 0x7632);
+        s.lo[i] = __byte_perm(l[2 * i], l[2 * i + 1], 0x7632);
+    }
+    return s;
+}
+
+// Infinities and NaN among bf16 pairs.  note: `seen` becomes nonzero (0 times
+// one is NaN); mask: ones over each value that is finite.
+__device__ __forceinline__ void note_nonfinite(uint32_t &seen, uint32_t pair)
+{
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(seen) : "r"(pair), "r"(0u));
+}
+__device__ __forceinline__ uint32_t finite_mask(uint32_t pair)
+{
+    return ((pair & 0x7F80u) != 0x7F80u ? 0xFFFFu : 0u) |
+           ((pair & 0x7F800000u) != 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+// An infinity or NaN is its own `hi`: the rest of it, infinity less infinity,
+// would be NaN.
+__device__ __forceinline__ void drop_rest(Split &s, int pair)
+{
+    const uint32_t keep = finite_mask(s.hi[pair]);
+    s.mid[pair] &= keep;
+    s.lo[pair] &= keep;
 }
 
 // Two fp32 values rounded to a bf16 pair.
@@ -522,7 +558,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
         // ---- add the halves of the CTAs of the cluster in rank order: every
         // CTA finishes a share of the (token, four ranks) entries
         const int quads = ranks / 4;
-        uint4 out{}, *to = nullptr;   // stored behind the arrival, which would wait for it
+        float4 out{}, *to = nullptr;   // stored behind the arrival, which would wait for it
         for (int e = tid * csize + crank; e < n * quads; e += kShrinkWarps * 32 * csize) {
             const int c = e / quads, q = e % quads;
             const float *mine = tile + c * ST + 4 * q;
@@ -536,16 +572,10 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
                     s.z += v.z;
                     s.w += v.w;
                 }
-            uint32_t hi[4], lo[4];
-            split_bf16(s.x * sc, hi[0], lo[0]);
-            split_bf16(s.y * sc, hi[1], lo[1]);
-            split_bf16(s.z * sc, hi[2], lo[2]);
-            split_bf16(s.w * sc, hi[3], lo[3]);
             if (to)
                 *to = out;
             to = p.T + (size_t)(m0 + list[begin + c]) * (p.R / 4) + r0 / 4 + q;
-            out = make_uint4(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16), lo[0] | (lo[1] << 16),
-                             lo[2] | (lo[3] << 16));
+            out = make_float4(s.x * sc, s.y * sc, s.z * sc, s.w * sc);
         }
         cluster_arrive();   // the tiles are read before the next item's
         if (to)
@@ -867,7 +897,18 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             const uint32_t st = base + slot * C::kStage;
             const int2 row = make_int2(g < q.x ? parts[slot].rows[g] : -1,
                                        g + 8 < q.x ? parts[slot].rows[g + 8] : -1);
-            const uint4 y[2] = {lds128a(st + yoff), lds128a(st + yoff + 8 * C::kYRow)};
+            uint32_t w[2][4];
+            auto load_y = [&] {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint4 y = lds128a(st + yoff + 8 * r * C::kYRow);
+                    w[r][0] = y.x;
+                    w[r][1] = y.y;
+                    w[r][2] = y.z;
+                    w[r][3] = y.w;
+                }
+            };
+            load_y();
             if (q.y) {   // new B
                 // column (row of B) and ranks of this lane.  S = 1: four
                 // consecutive ranks 4 t; else eight, 32 q + 8 t, for two steps
@@ -893,35 +934,52 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                     }
                 }
             }
-            uint32_t w[2][4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                w[r][0] = y[r].x;
-                w[r][1] = y[r].y;
-                w[r][2] = y[r].z;
-                w[r][3] = y[r].w;
-            }
             if (!q.z) {   // with an adapter
                 float acc[4][4];
+                uint32_t seen = 0;   // an infinity or NaN in T
+                auto multiply = [&](auto careful) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][e] = __uint_as_float(e & 1 ? w[e >> 1][i] & 0xFFFF0000u
-                                                          : w[e >> 1][i] << 16);
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][e] = __uint_as_float(e & 1 ? w[e >> 1][i] & 0xFFFF0000u
+                                                              : w[e >> 1][i] << 16);
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const int r4 = S == 1 ? t : 8 * (s / 2) + 2 * t + (s & 1);   // rank / 4
-                    uint4 ta = make_uint4(0u, 0u, 0u, 0u), tb = ta;
-                    if (r4 < quads) {
-                        ta = lds128a(st + toff + 16 * r4);
-                        tb = lds128a(st + toff + (8 * quads + r4) * 16);
+                    for (int s = 0; s < S; ++s) {
+                        const int r4 = S == 1 ? t : 8 * (s / 2) + 2 * t + (s & 1);   // rank / 4
+                        uint4 ta = make_uint4(0u, 0u, 0u, 0u), tb = ta;
+                        if (r4 < quads && row.x >= 0)
+                            ta = lds128a(st + toff + 16 * r4);
+                        if (r4 < quads && row.y >= 0)
+                            tb = lds128a(st + toff + (8 * quads + r4) * 16);
+                        Split u = split_f32(ta), v = split_f32(tb);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (decltype(careful)::value) {
+                                drop_rest(u, h);
+                                drop_rest(v, h);
+                            } else {
+                                note_nonfinite(seen, u.hi[h]);
+                                note_nonfinite(seen, v.hi[h]);
+                            }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16_16816(acc[i], u.hi[0], v.hi[0], u.hi[1], v.hi[1], b[i][s][0],
+                                           b[i][s][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16_16816(acc[i], u.mid[0], v.mid[0], u.mid[1], v.mid[1],
+                                           b[i][s][0], b[i][s][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16_16816(acc[i], u.lo[0], v.lo[0], u.lo[1], v.lo[1], b[i][s][0],
+                                           b[i][s][1]);
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mma_bf16_16816(acc[i], ta.x, tb.x, ta.y, tb.y, b[i][s][0], b[i][s][1]);
-                        mma_bf16_16816(acc[i], ta.z, tb.z, ta.w, tb.w, b[i][s][0], b[i][s][1]);
-                    }
+                };
+                multiply(std::false_type());
+                if (__any_sync(0xffffffffu, seen != 0)) {   // rare: once more, with care
+                    load_y();
+                    multiply(std::true_type());
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
@@ -1087,7 +1145,7 @@ cudaError_t launch_lora(const LoraPlan &pl, const LoraArgs &a, cudaStream_t stre
     p.scales = a.scales;
     p.index = a.index;
     p.hdr = static_cast<WsHeader *>(a.workspace);
-    p.T = reinterpret_cast<uint4 *>(p.hdr + 1);
+    p.T = reinterpret_cast<float4 *>(p.hdr + 1);
     p.ldx = a.ldx;
     p.ldy = a.ldy;
     p.ldo = a.ldo;

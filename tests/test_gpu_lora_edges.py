@@ -26,3 +26,61 @@ def test_lora_groups_of_few_and_of_many_tokens_in_turn(mxg, sizes, R):
         check(want, x, a, b, index, y, s)
         for _ in range(5):
             assert torch.equal(mxg.lora_add(x, a, b, index, y, scales=s), want)
+
+
+def one_adapter(a, b, x, y, N=40):
+    """lora_add of one adapter with the given ranks' weights: x [M][8], a
+    [R][8], b [R] and y [M] the same in every column."""
+    M = len(x)
+
+    def dev(v):
+        return torch.tensor(v, dtype=torch.float64, device=DEV).bfloat16()
+    bb = dev(b)[None, None, :].expand(1, N, len(b)).contiguous()
+    return (dev(x), dev(a)[None], bb, torch.zeros(M, dtype=torch.int32, device=DEV),
+            dev(y)[:, None].expand(M, N).contiguous())
+
+
+@pytest.mark.parametrize("M", [1, 9, 20])
+def test_lora_inner_products_keep_24_bits(mxg, M):
+    """Two ranks that cancel but for the last bits of an inner product: every
+    product and sum of the formula is exact, and so is the result."""
+    R = 8
+    for e in range(10, 24):
+        # out = 2 (1 + 2^-9 + 2^-e) - 2 (1 + 2^-9)
+        x = [[1.0, 2.0 ** -9, 2.0 ** -e, 0, 0, 0, 0, 0]] * M
+        a = [[0.0] * 8 for _ in range(R)]
+        a[0] = [1.0, 1.0, 1.0, 0, 0, 0, 0, 0]
+        a[5] = [1.0, 1.0, 0.0, 0, 0, 0, 0, 0]
+        b = [2.0, 0, 0, 0, 0, -2.0, 0, 0]
+        got = mxg.lora_add(*one_adapter(a, b, x, [0.0] * M))
+        assert (got.double() == 2.0 ** (1 - e)).all(), e
+
+
+@pytest.mark.parametrize("M", [1, 20, 70])
+def test_lora_infinite_inner_products(mxg, M):
+    """An infinity in x: the row's products are infinities of the factors'
+    signs, NaN where a zero meets it; the other rows keep their bits."""
+    inf = float("inf")
+    x, a, b, index, y, s = case(M, 72, 96, 24, 1, seed=M, index=torch.zeros(M))
+    clean = mxg.lora_add(x, a, b, index, y, scales=s)
+    row = M // 2
+    for value in (inf, -inf, float("nan")):
+        x2 = x.clone()
+        x2[row] = 0.0
+        x2[row, 5] = value
+        a2 = a.clone()
+        a2[0, :, 5] = 0.0                    # T = NaN in every rank ...
+        got = mxg.lora_add(x2, a2, b, index, y, scales=s)
+        assert got[row].isnan().all()
+        a2[0, :, 5] = 1.0                    # ... and +-inf in every rank
+        b2 = b.abs() + 1.0
+        got = mxg.lora_add(x2, a2, b2, index, y, scales=s)
+        want = torch.full_like(y[row], value)
+        assert torch.equal(got[row].isnan(), want.isnan())
+        assert value != value or torch.equal(got[row], want)
+        b2[0, 3, 7] = -1.0                   # one of the other sign: inf - inf
+        got = mxg.lora_add(x2, a2, b2, index, y, scales=s)
+        assert got[row, 3].isnan() and (value != value or torch.equal(got[row, 4:], want[4:]))
+        others = torch.arange(M, device=DEV) != row
+        got = mxg.lora_add(x2, a, b, index, y, scales=s)
+        assert torch.equal(got[others], clean[others])
