@@ -378,6 +378,7 @@ MXG_API int bf16_gemm_small_ex(const void *X, const void *W, int M, int N, int K
  *           call reads.  Not the workspace of a call that may run at the same
  *           time, nor one that a GEMM uses (those keep their counters in it).
  * The inner products and all sums are held in fp32; Out is rounded once.
+ * Infinities and NaN in any operand come out as in fp32 arithmetic.
  * Bitwise reproducible.  Unlike the GEMMs, nothing is read before the previous
  * kernel on `stream` has completed: A, B and index may be what it writes.
  * 1 <= M <= 2097088; K, N, R >= 8 and multiples of 8; R <= 128;

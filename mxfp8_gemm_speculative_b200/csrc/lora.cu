@@ -219,6 +219,17 @@ __device__ __forceinline__ void drop_rest(Split &s, int pair)
     s.lo[pair] &= keep;
 }
 
+// Values too small for a bf16 other than 0 become its smallest: an infinity
+// times them is an infinity, not NaN.
+__device__ __forceinline__ void lift(uint4 &v)
+{
+    uint32_t *b[4] = {&v.x, &v.y, &v.z, &v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if ((*b[i] & 0x7FFF0000u) == 0 && (*b[i] & 0xFFFFu) != 0)
+            *b[i] = (*b[i] & 0x80000000u) | 0x10000u;
+}
+
 // Two fp32 values rounded to a bf16 pair.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
@@ -883,6 +894,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
 #pragma unroll
             for (int s = 0; s < S; ++s)
                 b[i][s][0] = b[i][s][1] = 0;
+        uint32_t b_seen = 0;   // an infinity or NaN in this lane's B
         const uint32_t base = smem_u32(dyn);
         const int ncol = n0 + warp * 32 + 8 * t;
         const bool col_in = ncol < p.N;
@@ -933,10 +945,19 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                         }
                     }
                 }
+                b_seen = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (warp * 32 + 8 * (g >> 1) + 2 * i + (g & 1) < cols)   // else not B's
+#pragma unroll
+                        for (int s = 0; s < S; ++s) {
+                            note_nonfinite(b_seen, b[i][s][0]);
+                            note_nonfinite(b_seen, b[i][s][1]);
+                        }
             }
             if (!q.z) {   // with an adapter
                 float acc[4][4];
-                uint32_t seen = 0;   // an infinity or NaN in T
+                uint32_t seen = b_seen;   // an infinity or NaN in B or T
                 auto multiply = [&](auto careful) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -952,6 +973,10 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                             ta = lds128a(st + toff + 16 * r4);
                         if (r4 < quads && row.y >= 0)
                             tb = lds128a(st + toff + (8 * quads + r4) * 16);
+                        if (decltype(careful)::value) {
+                            lift(ta);
+                            lift(tb);
+                        }
                         Split u = split_f32(ta), v = split_f32(tb);
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
@@ -966,14 +991,24 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
                         for (int i = 0; i < 4; ++i)
                             mma_bf16_16816(acc[i], u.hi[0], v.hi[0], u.hi[1], v.hi[1], b[i][s][0],
                                            b[i][s][1]);
+                        // an infinity in B times `hi` is the product: 0 or a
+                        // rest of the other sign would make it NaN
+                        uint32_t bf[4][2];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_bf16_16816(acc[i], u.mid[0], v.mid[0], u.mid[1], v.mid[1],
-                                           b[i][s][0], b[i][s][1]);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                bf[i][h] = decltype(careful)::value
+                                               ? b[i][s][h] & finite_mask(b[i][s][h])
+                                               : b[i][s][h];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_bf16_16816(acc[i], u.lo[0], v.lo[0], u.lo[1], v.lo[1], b[i][s][0],
-                                           b[i][s][1]);
+                            mma_bf16_16816(acc[i], u.mid[0], v.mid[0], u.mid[1], v.mid[1], bf[i][0],
+                                           bf[i][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16_16816(acc[i], u.lo[0], v.lo[0], u.lo[1], v.lo[1], bf[i][0],
+                                           bf[i][1]);
                     }
                 };
                 multiply(std::false_type());

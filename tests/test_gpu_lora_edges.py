@@ -84,3 +84,59 @@ def test_lora_infinite_inner_products(mxg, M):
         others = torch.arange(M, device=DEV) != row
         got = mxg.lora_add(x2, a, b, index, y, scales=s)
         assert torch.equal(got[others], clean[others])
+
+
+@pytest.mark.parametrize("R", [8, 16, 40, 64, 128])
+@pytest.mark.parametrize("M", [1, 20, 70])
+def test_lora_infinite_weights(mxg, M, R):
+    """Infinities and NaN in one adapter's B: what 64 bits make of them, in its
+    column and its adapter's tokens; every other output keeps its bits.  The
+    last column tile has fewer columns than a full one."""
+    inf, nan = float("inf"), float("nan")
+    x, a, b, index, y, s = case(M, 72, 296, R, 2, seed=M + R, index=torch.arange(M) % 2)
+    clean = mxg.lora_add(x, a, b, index, y, scales=s)
+    b2 = b.clone()
+    b2[0, 5, 3], b2[0, 6, R - 1], b2[0, 7, 0] = inf, -inf, nan
+    b2[0, 260, 1], b2[0, 260, 4] = inf, -inf          # either inf, -inf or, of unlike signs, NaN
+    got = mxg.lora_add(x, a, b2, index, y, scales=s)
+    cols = [5, 6, 7, 260]
+    mine = index == 0
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[mine.nonzero(), torch.tensor(cols, device=DEV)] = False
+    assert torch.equal(got[keep], clean[keep])
+    inner = x[mine].double() @ a[0].double().T
+    want = torch.stack([y[mine, c].double() + float(s[0]) * (inner * b2[0, c].double()).sum(1)
+                        for c in cols], 1)
+    have = got[mine][:, cols].double()
+    assert not want.isfinite().any() and torch.equal(have.isnan(), want.isnan())
+    assert torch.equal(have[~have.isnan()], want[~want.isnan()])
+
+
+def test_lora_infinite_weights_and_zeros(mxg):
+    """Infinity times an inner product of 0 is NaN, times one of 2^-140 it is
+    an infinity; an infinite product stays one whatever the last bits of the
+    inner product (1 - 2^-9 + 2^-20: parts of either sign)."""
+    inf = float("inf")
+    a = [[0.0] * 8 for _ in range(8)]
+    a[2] = [1.0, -1.0, 1.0, 2.0 ** -70, 0, 0, 0, 0]
+    for row, sign in (([0.0] * 8, 0), ([0, 0, 0, 2.0 ** -70, 0, 0, 0, 0], 1),
+                      ([0, 0, 0, -2.0 ** -70, 0, 0, 0, 0], -1),
+                      ([1.0, 2.0 ** -9, 2.0 ** -20, 0, 0, 0, 0, 0], 1),
+                      ([-1.0, -2.0 ** -9, 2.0 ** -20, 0, 0, 0, 0, 0], -1),
+                      ([2.0 ** 127, 0, 0, 0, 0, 0, 0, 0], 1), ([-1.0, 0, 0, 0, 0, 0, 0, 0], -1)):
+        b = [0.0, 0, inf, 0, 0, 0, 0, 0]
+        got = mxg.lora_add(*one_adapter(a, b, [row], [3.0]))
+        if sign == 0:
+            assert got.isnan().all(), row
+        else:
+            assert (got == sign * inf).all(), row
+
+
+def test_lora_largest_inner_products(mxg):
+    """An inner product above the largest bf16 (and in fp32) times a small
+    weight is finite."""
+    a = [[0.0] * 8 for _ in range(8)]
+    a[1] = [1.0, 1.0, 0, 0, 0, 0, 0, 0]
+    x = [[255 * 2.0 ** 120, 2.0 ** 119, 0, 0, 0, 0, 0, 0]]     # above 255 2^120, the largest bf16
+    got = mxg.lora_add(*one_adapter(a, [0, 2.0 ** -127, 0, 0, 0, 0, 0, 0], x, [0.0]))
+    assert (got.double() == 2.0).all()       # 255.5 / 128 rounds to 2
