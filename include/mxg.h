@@ -390,6 +390,14 @@ MXG_API int lora_add(const void *X, long long ldx, const void *A, const void *B,
                long long ldo, int M, int N, int K, int R, int L, void *workspace,
                size_t workspace_bytes, cudaStream_t stream);
 
+/* The first error that any lora_add has recorded on the current device since
+ * the last reset, whatever workspace it ran in: *status is MXG_OK or
+ * MXG_ERR_TIMEOUT (a bounded wait ran out and the call's Out is not right).
+ * With reset = 1 it is cleared.  Stream-ordered on `stream` (behind the calls
+ * queued there) and synchronizes it; MXG_ERR_CAPTURE inside a capture.
+ * reset other than 0 or 1, or a NULL status: MXG_ERR_INVALID_ARG. */
+MXG_API int lora_status(int *status, int reset, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- sampling */
 
 /* One token per row of logits (the output of a vocabulary head), from a given
@@ -463,6 +471,9 @@ MXG_API int mxg_selftest_stream_ring(int bits, int M, int N, int K, int group_si
  * NULL for the static scratch array of w4a16_gemm_static_scratch on the
  * current device (read and clear it with w4a16_static_scratch_status). */
 MXG_API int mxg_selftest_wait_timeout(void *workspace, int limit_us, cudaStream_t stream);
+
+/* The same for what lora_status reports. */
+MXG_API int mxg_selftest_lora_wait_timeout(int limit_us, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -74,6 +74,8 @@ _SIGS = {
     "bf16_gemm_small_ex": (_i, [_p, _p, _i, _i, _i, _p, _p, _sz, _p, _p]),
     "lora_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "lora_add": (_i, [_p, _ll, _p, _p, _p, _p, _p, _ll, _p, _ll, _i, _i, _i, _i, _i, _p, _sz, _p]),
+    "lora_status": (_i, [_p, _i, _p]),
+    "mxg_selftest_lora_wait_timeout": (_i, [_i, _p]),
     "sample_logits": (_i, [_p, _i, _ll, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -841,7 +843,8 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Ten
     with i = index[m], for x bf16 [M][K], a bf16 [L][R][K], b bf16 [L][N][R],
     scales fp32 [L] (None: 1) and index int32 [M]; a token whose index is
     outside 0 .. L-1 (say -1) keeps its y.  ``out=y`` adds in place.  The rows
-    of x, y and out may be strided (a column range of a fused projection)."""
+    of x, y and out may be strided (a column range of a fused projection).
+    A bounded wait that ran out is reported by ``lora_status``."""
     args, out, keep = _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream)
     _dev_call(x.device, "lora_add", _lib.lora_add, *args, stream=stream)
     return out
@@ -855,6 +858,18 @@ def prepare_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: t
     args, out, keep = _lora_args(x, a, b, index, y, scales, out, workspace_buf, stream)
     return PreparedCall(_lib.lora_add, args + (_stream(stream, x.device),), "lora_add", keep,
                         x.device), out
+
+
+def lora_status(reset: bool = False, stream=None, device=None) -> int:
+    """0, or the first error (MXG_ERR_TIMEOUT) that any lora_add has recorded
+    on ``device`` (default: the current device) since the last reset, whatever
+    workspace it ran in.  Synchronizes the stream."""
+    dev = torch.device("cuda", torch.cuda.current_device() if device is None else
+                       torch.device(device).index)
+    v = ctypes.c_int(0)
+    _dev_call(dev, "lora_status", _lib.lora_status, ctypes.byref(v), 1 if reset else 0,
+              stream=stream)
+    return v.value
 
 
 # ---------------------------------------------------------------- sampling
@@ -974,6 +989,14 @@ def mxg_selftest_wait_timeout(workspace_buf: torch.Tensor | None, limit_us: int,
     _need_header(workspace_buf)
     _dev_call(workspace_buf.device, "mxg_selftest_wait_timeout", _lib.mxg_selftest_wait_timeout,
               _ptr(workspace_buf), int(limit_us), stream=stream)
+
+
+def mxg_selftest_lora_wait_timeout(limit_us: int, stream=None, device=None) -> None:
+    """The same for what ``lora_status`` reports on ``device``."""
+    dev = torch.device("cuda", torch.cuda.current_device() if device is None else
+                       torch.device(device).index)
+    _dev_call(dev, "mxg_selftest_lora_wait_timeout", _lib.mxg_selftest_lora_wait_timeout,
+              int(limit_us), stream=stream)
 
 
 def w4a16_static_scratch_status(reset: bool = False, stream=None, device=None) -> int:

@@ -573,6 +573,28 @@ int lora_add(const void *X, long long ldx, const void *A, const void *B, const f
     return to_status(launch_lora(pl, a, stream));
 }
 
+int lora_status(int *status, int reset, cudaStream_t stream)
+{
+    if (!status || (reset != 0 && reset != 1))
+        return MXG_ERR_INVALID_ARG;
+    if (current_device() < 0)
+        return MXG_ERR_CUDA;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess)
+        return MXG_ERR_CUDA;
+    if (cs != cudaStreamCaptureStatusNone)
+        return MXG_ERR_CAPTURE;
+    void *header = nullptr;
+    int v = 0;
+    if (lora_error_header(&header) != cudaSuccess ||
+        cudaMemcpyAsync(&v, header, sizeof(int), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+        (reset && cudaMemsetAsync(header, 0, sizeof(WsHeader), stream) != cudaSuccess) ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+        return MXG_ERR_CUDA;
+    *status = v;
+    return MXG_OK;
+}
+
 int sample_logits(const void *logits, int dtype, long long ld, int M, int V, const float *u,
                   const float *temperature, const int *top_k, const float *top_p,
                   const float *min_p, int *tokens, float *probs, cudaStream_t stream)
@@ -658,6 +680,13 @@ int mxg_selftest_wait_timeout(void *workspace, int limit_us, cudaStream_t stream
             return st;
     }
     return to_status(launch_wait_timeout_selftest(workspace, limit_us, stream));
+}
+
+int mxg_selftest_lora_wait_timeout(int limit_us, cudaStream_t stream)
+{
+    if (limit_us < 1 || limit_us > 10000000)
+        return MXG_ERR_INVALID_ARG;
+    return to_status(launch_lora_wait_timeout(limit_us, stream));
 }
 
 size_t bf16_gemm_small_workspace_bytes(int M, int N, int K)

@@ -135,6 +135,8 @@ bool lora_shape_ok(int M, int N, int K, int R);
 size_t lora_scratch_bytes(int M, int R);   // status header and the [M][R] inner products
 LoraPlan plan_lora(int device, int M, int N, int K, int R);   // of a shape that is ok
 cudaError_t launch_lora(const LoraPlan &plan, const LoraArgs &args, cudaStream_t stream);
+cudaError_t lora_error_header(void **header);   // of the current device
+cudaError_t launch_lora_wait_timeout(int limit_us, cudaStream_t stream);
 
 // --------------------------------------------------------------- sampling
 struct SamplePlan {

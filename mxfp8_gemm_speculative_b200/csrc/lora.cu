@@ -55,6 +55,30 @@ struct LoraParams {
     int M, N, K, R, L;
 };
 
+// The first wait that ran out in any call on the device since lora_status
+// cleared it: the workspace of a call may be gone when the caller asks.
+__device__ WsHeader g_lora_errors;
+
+__device__ __forceinline__ void record_timeout(WsHeader *hdr, int where)
+{
+    record_error(hdr, MXG_ERR_TIMEOUT, where);
+    record_error(&g_lora_errors, MXG_ERR_TIMEOUT, where);
+}
+
+// A wait that nothing ends, for the self-test of that record.
+__global__ void lora_wait_timeout_kernel(unsigned long long limit_ns)
+{
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(&bar, 0, limit_ns));
+    if (!ok && threadIdx.x == 0)
+        record_timeout(&g_lora_errors, 599);
+}
+
 // 16 bytes global -> shared, asynchronous; zeros when `in` is false.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in)
 {
@@ -425,7 +449,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
             return;
         ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs));
         if (!ok && lane == 0)
-            record_error(p.hdr, MXG_ERR_TIMEOUT, where);
+            record_timeout(p.hdr, where);
     };
 
     if (warp == kShrinkWarps) {
@@ -747,7 +771,7 @@ __global__ void __launch_bounds__(Expand<S>::kThreads, S <= 2 ? 3 : (S == 4 ? 2 
             return;
         ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs));
         if (!ok && lane == 0)
-            record_error(p.hdr, MXG_ERR_TIMEOUT, where);
+            record_timeout(p.hdr, where);
     };
 
     if (warp == C::kConsumers) {
@@ -1167,6 +1191,17 @@ LoraPlan plan_lora(int device, int M, int N, int K, int R)
         pl.expand_shares = (int)(pl.expand_subs * blocks);
     }
     return pl;
+}
+
+cudaError_t lora_error_header(void **header)
+{
+    return cudaGetSymbolAddress(header, g_lora_errors);
+}
+
+cudaError_t launch_lora_wait_timeout(int limit_us, cudaStream_t stream)
+{
+    lora_wait_timeout_kernel<<<1, 32, 0, stream>>>((unsigned long long)limit_us * 1000ull);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_lora(const LoraPlan &pl, const LoraArgs &a, cudaStream_t stream)
