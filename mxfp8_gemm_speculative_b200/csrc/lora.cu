@@ -280,7 +280,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // in the batch changes the order of its sums.
 template <int RT>
 struct Shrink {
-    static constexpr int kTok = kBlockTok;                  // tokens of a group at a time
+    static constexpr int kTok = kBlockTok;                  // most tokens of a group
     static constexpr int sub(int rows) { return (rows + 16 * RT) * 128; }   // 64 k of tokens, ranks
     static constexpr int kSubMany = RT == 1 ? 2 : 1, kSubFew = RT == 1 ? 4 : 2;   // per stage
     static constexpr int kMany = kSubMany * sub(kTok), kFewStage = kSubFew * sub(kFew);
@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
     const int k1 = min(p.K, (int)((long long)(crank + 1) * units / csize) * 64);
 
     // Every warp walks the items of this cluster, in the same order: every
-    // gridDim.y-th group of the block that has an adapter, kTok tokens at a
-    // time.  Each ends with two cluster barriers that all threads take part in.
+    // gridDim.y-th group of the block that has an adapter.  Each ends with two
+    // cluster barriers that all threads take part in.
     // (The lanes pick the groups at once: a walk that counts them costs 380
     // cycles a group, 5 us before the 24th one's first copy.)
     u64 rest;
@@ -428,17 +428,13 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
         const unsigned mine1 = __ballot_sync(0xffffffffu, lead1 && n1 % gridDim.y == blockIdx.y);
         rest = mine0 | (u64)mine1 << 32;
     }
-    int a = -1, ntok = 0, begin = 0;
+    int a = -1, ntok = 0;
     auto next_item = [&]() {
-        begin += C::kTok;
-        if (begin < ntok)
-            return true;
         if (rest == 0)
             return false;
         const int first = __ffsll(rest) - 1;
         rest &= rest - 1;
         ntok = take_group(grp, first, list, lane, a);
-        begin = 0;
         return true;
     };
     // waits by whole warps; after one that ran out the role only goes through
@@ -472,10 +468,9 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
             constexpr int kRows = kIsFew ? kFew : C::kTok;
             constexpr int kSub = kIsFew ? C::kSubFew : C::kSubMany;
             constexpr int kFours = kRows / 4;
-            const int n = min(C::kTok, ntok - begin);
-            const int m = m0 + list[begin];
+            const int n = ntok, m = m0 + list[0];
             // boxes of 16 tokens, for a run (a few rows are as well copied one by one)
-            const bool run = !kIsFew && m0 + list[begin + n - 1] - m == n - 1;
+            const bool run = !kIsFew && m0 + list[n - 1] - m == n - 1;
             const int xb = run ? (n + 15) / 16 : 0;
             const int fours = run ? 0 : (n + 3) / 4;
             // few: rows lane / 8 + 4 i, their 16 bytes lane % 8; else gathers
@@ -488,13 +483,13 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < kFours; ++i) {
                     const int r = (lane >> 3) + 4 * i;
-                    src[i] = p.X + (m0 + list[begin + (r < n ? r : 0)]) * p.ldx + 8 * c;
+                    src[i] = p.X + (m0 + list[r < n ? r : 0]) * p.ldx + 8 * c;
                     dst[i] = r * 128 + ((c ^ (r & 7)) << 4);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    row[i] = m0 + list[begin + min(4 * (lane % kFours) + i, n - 1)];
+                    row[i] = m0 + list[min(4 * (lane % kFours) + i, n - 1)];
             }
             const int arow = a * p.R + r0;
             int s = 0;
@@ -559,7 +554,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
             }
         };
         while (next_item()) {
-            if (min(C::kTok, ntok - begin) <= kFew)
+            if (ntok <= kFew)
                 stages(std::true_type());
             else
                 stages(std::false_type());
@@ -581,7 +576,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
     uint32_t phase = 0;
     auto wait_full = [&](int s, uint32_t parity) { wait_on(&full[s], parity, 541); };
     while (next_item()) {
-        const int n = min(C::kTok, ntok - begin);
+        const int n = ntok;
         const float sc = p.scales ? __ldcg(p.scales + a) : 1.f;   // ahead of its use
         if (n <= kFew)
             shrink_item<RT, kFew, C::kSubFew>(n, k0, k1, smem_u32(dyn), tile, empty, slot, phase,
@@ -609,7 +604,7 @@ __global__ void __launch_bounds__(Shrink<RT>::kThreads, 2)
                 }
             if (to)
                 *to = out;
-            to = p.T + (size_t)(m0 + list[begin + c]) * (p.R / 4) + r0 / 4 + q;
+            to = p.T + (size_t)(m0 + list[c]) * (p.R / 4) + r0 / 4 + q;
             out = make_float4(s.x * sc, s.y * sc, s.z * sc, s.w * sc);
         }
         cluster_arrive();   // the tiles are read before the next item's
