@@ -8,10 +8,12 @@
 // What bounds it: 2 M R (K + N) flops against the bytes of the adapters in
 // use (2 R (K + N) each) and of X, Y and Out.  With R <= 128 that is at most
 // a few hundred flops per byte for one adapter and far fewer for many, so
-// HBM bytes bound a large batch and latency a small one.  mma.sync is enough:
-// its pipe was 8 % busy in the expand kernel of a prefill chunk (8192 tokens,
-// R = 16), and a tcgen05 tile (128 rows of one adapter) would be mostly empty
-// in a decode batch.
+// HBM bytes should bound a large batch, and latency bounds a small one.
+// mma.sync, since a tcgen05 tile (128 rows of one adapter) would be mostly
+// empty in a decode batch.  In the expand kernel of a prefill chunk its pipe is
+// 24 % busy at R = 16, 37 % at R = 32 and 47 % at R = 128, and the one that
+// takes T apart (logic and permutes) 50 %: from R = 32 on those two, and not
+// bytes, are what the kernel takes its time for.
 //
 // Two kernels, joined by programmatic dependent launch:
 //   shrink   T = s * X A^T, [M][R] in fp32;
@@ -25,9 +27,10 @@
 // block that uses it and once in all for up to 64 tokens.
 //
 // Measured (B200, graph of calls over rotating buffers): 8192 tokens,
-// 5120 -> 17408, R = 16: 128 us for 658 MB (5.1 TB/s; shrink 23, expand 105);
-// 37 tokens of 48 adapters, 17408 -> 5120, R = 64: 23 us for 72 MB; one token,
-// 5120 -> 5120: 6.8 us (two kernels of a few dependent steps each).
+// 5120 -> 17408, R = 16: 132 us for 658 MB (5.0 TB/s; shrink 23, expand 109),
+// R = 32: 172 us; 37 tokens of 48 adapters, 17408 -> 5120, R = 64: 23 us for
+// 72 MB; one token, 5120 -> 5120: 6.9 us (two kernels of a few dependent steps
+// each).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
